@@ -525,6 +525,293 @@ nq_status nq_entropy_decode(const uint16_t* words, const uint32_t* offsets, cons
                      "nq_entropy_decode launch");
 }
 
+// Whether [p, p + n) and [q, q + m) share a byte (either may be empty or NULL).
+static bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  if (!p || !q || n == 0 || m == 0) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
+}
+
+nq_status nq_page_tables(const int32_t* lens, const int32_t* counts, int requests, int page_size,
+                         const int32_t* free_pages, int64_t n_free, const int32_t* taken,
+                         int32_t* table, int64_t table_stride, int32_t* lens_out, int32_t* starts, int32_t* slots,
+                         int32_t* positions, int64_t max_rows, int32_t* used,
+                         nq_stream_t stream) {
+  if (requests < 0 || page_size < 1 || n_free < 0 || max_rows < 0 || table_stride < 1)
+    return fail(NQ_ERR_INVALID, "need requests >= 0, page_size >= 1, table_stride >= 1, "
+                                "n_free >= 0, max_rows >= 0");
+  if (requests > NQ_PAGE_TABLES_MAX_REQUESTS || page_size > 65536 ||
+      table_stride > (int64_t(1) << 24) || max_rows > 0x7FFFFFFF)
+    return fail(NQ_ERR_UNSUPPORTED, "requests <= %d, page_size <= 65536, table_stride <= 2^24, "
+                                    "max_rows < 2^31", NQ_PAGE_TABLES_MAX_REQUESTS);
+  if (!starts || !used || !aligned(starts, 4) || !aligned(used, 4))
+    return fail(NQ_ERR_INVALID, "starts or used NULL or misaligned");
+  if (requests > 0 && (!lens || !counts || !table || !lens_out || !aligned(lens, 4) ||
+                       !aligned(counts, 4) || !aligned(table, 4) || !aligned(lens_out, 4)))
+    return fail(NQ_ERR_INVALID, "lens, counts, table or lens_out NULL or misaligned");
+  if (n_free > 0 && (!free_pages || !aligned(free_pages, 4)))
+    return fail(NQ_ERR_INVALID, "free_pages NULL or misaligned");
+  if (max_rows > 0 && (!slots || !positions || !aligned(slots, 4) || !aligned(positions, 4)))
+    return fail(NQ_ERR_INVALID, "slots or positions NULL or misaligned");
+  const size_t rb = static_cast<size_t>(requests) * 4, mb = static_cast<size_t>(max_rows) * 4;
+  if (taken && !aligned(taken, 4)) return fail(NQ_ERR_INVALID, "taken misaligned");
+  const struct { const void* p; size_t n; } in[5] = {
+      {taken, 4}, {lens, rb}, {counts, rb}, {free_pages, static_cast<size_t>(n_free) * 4},
+      {table, rb * static_cast<size_t>(table_stride)}};
+  const struct { const void* p; size_t n; } out[6] = {
+      {lens_out, rb}, {starts, rb + 4}, {slots, mb}, {positions, mb}, {used, 8},
+      {table, rb * static_cast<size_t>(table_stride)}};
+  for (int o = 0; o < 6; ++o) {
+    for (int i = 0; i < (o == 5 ? 4 : 5); ++i)
+      if (overlap(out[o].p, out[o].n, in[i].p, in[i].n))
+        return fail(NQ_ERR_INVALID, "an output overlaps lens, counts, free_pages, taken or table");
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o].p, out[o].n, out[i].p, out[i].n))
+        return fail(NQ_ERR_INVALID, "two outputs overlap");
+  }
+  nq::PageTablesLaunch L{lens,     counts, requests, page_size, free_pages, n_free, taken, table,
+                         table_stride, lens_out, starts, slots, positions, max_rows, used};
+  return cuda_status(nq::launch_page_tables(L, reinterpret_cast<cudaStream_t>(stream)),
+                     "nq_page_tables launch");
+}
+
+static nq_status check_rows(const void* p, nq_kv_strides s, int type, const char* name) {
+  if (type != NQ_BF16 && type != NQ_F32)
+    return fail(NQ_ERR_INVALID, "%s: type must be NQ_BF16 or NQ_F32 (got %d)", name, type);
+  return check_kv(p, s, name);
+}
+
+// Output strides: a stride of 0 over more than one index would write one
+// vector from several rows.
+static nq_status check_out(const void* p, nq_kv_strides s, int64_t units, int64_t heads,
+                           int64_t rows, const char* name) {
+  if (nq_status st = check_kv(p, s, name)) return st;
+  if ((units > 1 && s.unit == 0) || (heads > 1 && s.head == 0) || (rows > 1 && s.token == 0))
+    return fail(NQ_ERR_INVALID, "%s: a stride of 0 over several rows of an output", name);
+  return NQ_OK;
+}
+
+nq_status nq_qk_norm_rope(const void* q, nq_kv_strides qs, int q_heads, const void* k,
+                          nq_kv_strides ks, int k_heads, int in_type, int units, int64_t rows,
+                          const float* q_weight, const float* k_weight, float eps,
+                          const int32_t* positions, int64_t pos_stride, int64_t pos_base,
+                          const float* rope_tab, int64_t rope_max_pos, void* q_out,
+                          nq_kv_strides qos, int q_type, void* k_out, nq_kv_strides kos,
+                          int k_type, nq_stream_t stream) {
+  if (units < 0 || rows < 0 || q_heads < 0 || k_heads < 0 || q_heads > 1024 || k_heads > 1024 ||
+      pos_base < 0)
+    return fail(NQ_ERR_INVALID, "need units, rows, pos_base >= 0 and 0 <= heads <= 1024");
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(NQ_ERR_INVALID, "eps must be finite and >= 0");
+  if (q_heads + k_heads == 0) return fail(NQ_ERR_INVALID, "q_heads and k_heads are both 0");
+  if (units == 0 || rows == 0) return NQ_OK;
+  if (rows > 0x7FFFFFFF / units || static_cast<int64_t>(units) * rows > 0x7FFFFFFF / (q_heads + k_heads))
+    return fail(NQ_ERR_UNSUPPORTED, "units * rows * heads must stay below 2^31");
+  if (q_heads > 0) {
+    if (nq_status st = check_rows(q, qs, in_type, "q")) return st;
+    if (nq_status st = check_rows(q_out, qos, q_type, "q_out")) return st;
+    if (nq_status st = check_out(q_out, qos, units, q_heads, rows, "q_out")) return st;
+    if (q_out == q && (q_type != in_type || qs.unit != qos.unit || qs.head != qos.head ||
+                       qs.token != qos.token))
+      return fail(NQ_ERR_INVALID, "q_out is q with other strides or another type");
+  }
+  if (k_heads > 0) {
+    if (nq_status st = check_rows(k, ks, in_type, "k")) return st;
+    if (nq_status st = check_rows(k_out, kos, k_type, "k_out")) return st;
+    if (nq_status st = check_out(k_out, kos, units, k_heads, rows, "k_out")) return st;
+    if (k_out == k && (k_type != in_type || ks.unit != kos.unit || ks.head != kos.head ||
+                       ks.token != kos.token))
+      return fail(NQ_ERR_INVALID, "k_out is k with other strides or another type");
+  }
+  if ((q_weight && !aligned(q_weight, 16)) || (k_weight && !aligned(k_weight, 16)))
+    return fail(NQ_ERR_INVALID, "weights must be 16-byte aligned");
+  if (nq_status st = check_rope(rope_tab, rope_max_pos)) return st;
+  if (positions) {
+    if (!aligned(positions, 4)) return fail(NQ_ERR_INVALID, "positions misaligned");
+    if (pos_stride < rows && units > 1 && pos_stride != 0)
+      return fail(NQ_ERR_INVALID, "pos_stride < rows");
+  } else if (pos_base + rows > rope_max_pos) {
+    return fail(NQ_ERR_INVALID, "positions up to %lld exceed rope_max_pos %lld",
+                static_cast<long long>(pos_base + rows - 1), static_cast<long long>(rope_max_pos));
+  }
+  nq::NormRopeLaunch L{};
+  L.q = q;
+  L.k = k;
+  L.qs = qs;
+  L.ks = ks;
+  L.q_heads = q_heads;
+  L.k_heads = k_heads;
+  L.in_f32 = in_type == NQ_F32;
+  L.q_f32 = q_type == NQ_F32;
+  L.k_f32 = k_type == NQ_F32;
+  L.units = units;
+  L.rows = rows;
+  L.q_weight = q_weight;
+  L.k_weight = k_weight;
+  L.eps = eps;
+  L.positions = positions;
+  L.pos_stride = pos_stride;
+  L.pos_base = pos_base;
+  L.rope_tab = rope_tab;
+  L.rope_max_pos = rope_max_pos;
+  L.q_out = q_out;
+  L.k_out = k_out;
+  L.qos = qos;
+  L.kos = kos;
+  return cuda_status(nq::launch_norm_rope(L, reinterpret_cast<cudaStream_t>(stream)),
+                     "nq_qk_norm_rope launch");
+}
+
+nq_status nq_encode_slots(const void* K, nq_kv_strides ks, const void* V, nq_kv_strides vs,
+                          int heads, int64_t rows, const int32_t* slots,
+                          const int32_t* positions, int page_size, int64_t pages,
+                          const float* rope_tab, int64_t rope_max_pos, const nq_packed* k_out,
+                          const nq_packed* v_out, nq_stream_t stream) {
+  if (!K && !V) return fail(NQ_ERR_INVALID, "K and V are both NULL");
+  if (heads < 1 || heads > 1024 || rows < 0 || page_size < 1 || pages < 0)
+    return fail(NQ_ERR_INVALID, "need 1 <= heads <= 1024, rows >= 0, page_size >= 1, pages >= 0");
+  if (rows == 0) return NQ_OK;
+  if (rows > 0x7FFFFFFF / heads || pages > 0x7FFFFFFF / page_size)
+    return fail(NQ_ERR_UNSUPPORTED, "rows * heads and pages * page_size must stay below 2^31");
+  if (!slots || !aligned(slots, 4)) return fail(NQ_ERR_INVALID, "slots NULL or misaligned");
+  const void* Kd = nullptr;
+  const void* Vd = nullptr;
+  if (K) {
+    if (nq_status st = check_kv(K, ks, "K")) return st;
+    if (nq_status st = check_packed(k_out, "k_out")) return st;
+    if (nq_status st = check_rope(rope_tab, rope_max_pos)) return st;
+    if (!positions || !aligned(positions, 4))
+      return fail(NQ_ERR_INVALID, "positions NULL or misaligned (required for keys)");
+    if (nq_status st = device_readable(K, &Kd, "K")) return st;
+  }
+  if (V) {
+    if (nq_status st = check_kv(V, vs, "V")) return st;
+    if (nq_status st = check_packed(v_out, "v_out")) return st;
+    if (nq_status st = device_readable(V, &Vd, "V")) return st;
+  }
+  nq::EncodeSlotsLaunch L{};
+  L.K = Kd;
+  L.ks = ks;
+  L.V = Vd;
+  L.vs = vs;
+  L.heads = heads;
+  L.rows = rows;
+  L.slots = slots;
+  L.positions = positions;
+  L.page_size = page_size;
+  L.pages = pages;
+  L.rope_tab = rope_tab;
+  L.rope_max_pos = rope_max_pos;
+  if (K) L.k_out = *k_out;
+  if (V) L.v_out = *v_out;
+  return cuda_status(nq::launch_encode_slots(L, reinterpret_cast<cudaStream_t>(stream)),
+                     "nq_encode_slots launch");
+}
+
+size_t nq_tree_attend_workspace_bytes(int units, int heads, int G, int nodes, int64_t n,
+                                      int shared) {
+  if (units < 0 || heads < 1 || G < 1 || nodes < 1 || n < 1) return 0;
+  return nq::tree_workspace_bytes(units, heads, G, nodes, n, shared != 0);
+}
+
+nq_status nq_tree_attend(const void* q, nq_kv_strides qs, const void* K_new, nq_kv_strides kns,
+                         const void* V_new, nq_kv_strides vns, int units, int heads, int G,
+                         int nodes, const nq_packed* k_in, const nq_packed* v_in, int64_t n,
+                         const int32_t* lens, const int32_t* table, int64_t table_stride,
+                         int page_size, int64_t pages, const int32_t* positions,
+                         int64_t pos_stride, int64_t pos_base, const float* rope_tab,
+                         int64_t rope_max_pos, const uint64_t* mask, int64_t mask_stride,
+                         float scale, void* out, nq_kv_strides os, float* lse, void* ws,
+                         size_t ws_bytes, nq_stream_t stream) {
+  if (units < 0 || heads < 1 || heads > 1024 || G < 1 || G > 8)
+    return fail(NQ_ERR_INVALID, "need units >= 0, 1 <= heads <= 1024, 1 <= G <= 8");
+  if (nodes < 1 || nodes > NQ_TREE_MAX_NODES)
+    return fail(NQ_ERR_INVALID, "need 1 <= nodes <= %d", NQ_TREE_MAX_NODES);
+  if (n < 0 || pos_base < 0) return fail(NQ_ERR_INVALID, "need n >= 0, pos_base >= 0");
+  if (!std::isfinite(scale)) return fail(NQ_ERR_INVALID, "scale must be finite");
+  if (units == 0) return NQ_OK;
+  if (nq_status st = check_kv(q, qs, "q")) return st;
+  if (nq_status st = check_kv(K_new, kns, "K_new")) return st;
+  if (nq_status st = check_kv(V_new, vns, "V_new")) return st;
+  if (nq_status st = check_out(out, os, units, static_cast<int64_t>(heads) * G, nodes, "out")) return st;
+  if (out == q || out == K_new || out == V_new)
+    return fail(NQ_ERR_INVALID, "out overlaps an input");
+  if (lse && !aligned(lse, 4)) return fail(NQ_ERR_INVALID, "lse misaligned");
+  if (lens && !aligned(lens, 4)) return fail(NQ_ERR_INVALID, "lens misaligned");
+  if (mask) {
+    if (!aligned(mask, 8)) return fail(NQ_ERR_INVALID, "mask misaligned");
+    const int64_t words = static_cast<int64_t>(nodes) * ((nodes + 63) / 64);
+    if (mask_stride != 0 && mask_stride < words && units > 1)
+      return fail(NQ_ERR_INVALID, "mask_stride must be 0 or at least nodes * ceil(nodes / 64)");
+  }
+  if (n > 0) {
+    if (nq_status st = check_packed(k_in, "k_in")) return st;
+    if (nq_status st = check_packed(v_in, "v_in")) return st;
+    if (nq_status st = check_rope(rope_tab, rope_max_pos)) return st;
+    if (positions) {
+      if (!aligned(positions, 4)) return fail(NQ_ERR_INVALID, "positions misaligned");
+      if (pos_stride < n && units > 1) return fail(NQ_ERR_INVALID, "pos_stride < n");
+    } else if (pos_base + n > rope_max_pos) {
+      return fail(NQ_ERR_INVALID, "positions up to %lld exceed rope_max_pos %lld",
+                  static_cast<long long>(pos_base + n - 1), static_cast<long long>(rope_max_pos));
+    }
+    if (table) {
+      if (!aligned(table, 4)) return fail(NQ_ERR_INVALID, "table misaligned");
+      if (page_size < 1 || pages < 0 || table_stride < 1)
+        return fail(NQ_ERR_INVALID, "need page_size >= 1, pages >= 0, table_stride >= 1");
+      if ((n + page_size - 1) / page_size > table_stride)
+        return fail(NQ_ERR_INVALID, "n tokens need %lld pages, a table row holds %lld",
+                    static_cast<long long>((n + page_size - 1) / page_size),
+                    static_cast<long long>(table_stride));
+    }
+    if (n > 0x7FFFFFFF || pos_base + n > 0x7FFFFFFF ||
+        nq::tree_ctas(units, heads, G, nodes, n) > 0x7FFFFFFF)
+      return fail(NQ_ERR_UNSUPPORTED, "n or units * heads * chunks too large for one launch");
+    if (!ws || !aligned(ws, 16))
+      return fail(NQ_ERR_INVALID, "workspace NULL or not 16-byte aligned");
+    const size_t need =
+        nq_tree_attend_workspace_bytes(units, heads, G, nodes, n, positions == nullptr);
+    if (ws_bytes < need)
+      return fail(NQ_ERR_WORKSPACE, "tree attention workspace too small: %zu < %zu", ws_bytes, need);
+  }
+  if (static_cast<int64_t>(units) * heads * G * nodes > 0x7FFFFFFF)
+    return fail(NQ_ERR_UNSUPPORTED, "units * heads * G * nodes must stay below 2^31");
+  nq::TreeLaunch L{};
+  L.q = q;
+  L.qs = qs;
+  L.K_new = K_new;
+  L.kns = kns;
+  L.V_new = V_new;
+  L.vns = vns;
+  L.units = units;
+  L.heads = heads;
+  L.G = G;
+  L.nodes = nodes;
+  if (n > 0) {
+    L.k_in = *k_in;
+    L.v_in = *v_in;
+  }
+  L.n = n;
+  L.lens = lens;
+  L.table = table;
+  L.table_stride = table_stride;
+  L.page_size = page_size;
+  L.pages = pages;
+  L.positions = positions;
+  L.pos_stride = pos_stride;
+  L.pos_base = pos_base;
+  L.rope_tab = rope_tab;
+  L.rope_max_pos = rope_max_pos;
+  L.mask = mask;
+  L.mask_stride = mask_stride;
+  L.scale = scale;
+  L.out = out;
+  L.os = os;
+  L.lse = lse;
+  L.ws = ws;
+  return cuda_status(nq::launch_tree_attend(L, reinterpret_cast<cudaStream_t>(stream)),
+                     "nq_tree_attend launch");
+}
+
 nq_status nq_set_decode_engine(int engine) {
   if (engine != NQ_DECODE_AUTO && engine != NQ_DECODE_TENSOR_CORES && engine != NQ_DECODE_CUDA_CORES)
     return fail(NQ_ERR_INVALID, "decode engine must be 0, 1 or 2 (got %d)", engine);

@@ -84,6 +84,11 @@ struct CodecArgs {
   FastDiv div_groups, div_stiles;
   int64_t pairs;  // encode: units * n (unit, slot) pairs, below 2^31
   FastDiv div_n;  // encode: division by n
+  // encode into given slots: row p of the one "unit" goes to slot slots[p] of
+  // pages of div_page.d slots, nslots in all; its RoPE position is idx[p]
+  const int32_t* slots;
+  FastDiv div_page;
+  int64_t nslots;
   // tensor-core decode: a tile holds tc_m slot tiles of one head group
   int tc_m;
   int64_t tc_sgroups;  // ceil(slot_tiles / tc_m)
@@ -141,10 +146,18 @@ struct EncPair {
   bool valid;
   int64_t unit, slot;
 };
+template <bool SLOTS>
 __device__ __forceinline__ EncPair enc_pair(const CodecArgs& a, int64_t p0, int slot_l) {
   EncPair e;
   const int64_t p = p0 + slot_l;
   e.valid = p < a.pairs;
+  if (SLOTS) {  // the row itself; rows whose slot is out of range are skipped
+    e.unit = 0;
+    e.slot = e.valid ? p : 0;
+    const int32_t s = __ldg(a.slots + e.slot);
+    e.valid = e.valid && s >= 0 && s < a.nslots;
+    return e;
+  }
   const uint32_t pp = static_cast<uint32_t>(e.valid ? p : 0);
   const uint32_t u = fdiv(pp, a.div_n);
   e.unit = u;
@@ -152,9 +165,27 @@ __device__ __forceinline__ EncPair enc_pair(const CodecArgs& a, int64_t p0, int 
   return e;
 }
 // Source token of a pair (its RoPE position is pos_base + src), -1 if invalid.
+template <bool SLOTS>
 __device__ __forceinline__ int32_t enc_src(const CodecArgs& a, const EncPair& e) {
   if (!e.valid) return -1;
+  if (SLOTS) return static_cast<int32_t>(e.slot);
   return a.idx ? __ldg(a.idx + e.unit * a.idx_stride + e.slot) : static_cast<int32_t>(e.slot);
+}
+
+// The RoPE position (minus pos_base) of a pair with source src.
+template <bool SLOTS>
+__device__ __forceinline__ int32_t enc_pos(const CodecArgs& a, const EncPair& e, int32_t src) {
+  if (!SLOTS || src < 0) return src;
+  const int32_t p = __ldg(a.idx + e.slot);
+  return p < 0 ? 0 : p;  // out-of-contract positions stay in bounds
+}
+// The vector of the packed store that a valid pair of head h is written to.
+template <bool SLOTS>
+__device__ __forceinline__ int64_t enc_vec(const CodecArgs& a, const EncPair& e, int h) {
+  if (!SLOTS) return e.unit * a.pu + h * a.ph + a.slot0 + e.slot;
+  const uint32_t s = static_cast<uint32_t>(e.valid ? __ldg(a.slots + e.slot) : 0);
+  const uint32_t page = fdiv(s, a.div_page);
+  return page * a.pu + h * a.ph + (s - page * a.div_page.d);
 }
 
 // ---------------------------------------------------------- E8 (fp32x2)
@@ -560,7 +591,7 @@ __device__ __forceinline__ void quantise_half(float2 (&v)[32], int half, bool va
   }
 }
 
-template <int BITS, bool ROPE, bool EXACT>
+template <int BITS, bool ROPE, bool EXACT, bool SLOTS>
 __global__ void __launch_bounds__(256, 2) encode_kernel(const CodecArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int nthreads = blockDim.x;
@@ -601,12 +632,14 @@ __global__ void __launch_bounds__(256, 2) encode_kernel(const CodecArgs a) {
 
   // prologue: tile 0 (rows + its RoPE table), then tile 1 in flight
   EncPair pp_pref{};
-  int32_t src_pref = -1;
+  int32_t src_pref = -1, pos_pref = -1;
   if (my_tiles > 0) {
     const EncTile t0 = tile(0);
-    const EncPair p0 = enc_pair(a, t0.p0, slot_l);
-    const int32_t s0 = enc_src(a, p0);
-    if (ROPE) issue_rope_rows(a.tab, a.n_a, a.pos_base, s0, raw, warp, nthreads / 32, lane);
+    const EncPair p0 = enc_pair<SLOTS>(a, t0.p0, slot_l);
+    const int32_t s0 = enc_src<SLOTS>(a, p0);
+    if (ROPE)
+      issue_rope_rows(a.tab, a.n_a, a.pos_base, enc_pos<SLOTS>(a, p0, s0), raw, warp,
+                      nthreads / 32, lane);
     issue_rows(t0, p0, s0, 0);
   }
   cp_async_commit();
@@ -616,9 +649,11 @@ __global__ void __launch_bounds__(256, 2) encode_kernel(const CodecArgs a) {
   sync();
   if (my_tiles > 1) {
     const EncTile t1 = tile(1);
-    const EncPair p1 = enc_pair(a, t1.p0, slot_l);
-    const int32_t s1 = enc_src(a, p1);
-    if (ROPE) issue_rope_rows(a.tab, a.n_a, a.pos_base, s1, raw, warp, nthreads / 32, lane);
+    const EncPair p1 = enc_pair<SLOTS>(a, t1.p0, slot_l);
+    const int32_t s1 = enc_src<SLOTS>(a, p1);
+    if (ROPE)
+      issue_rope_rows(a.tab, a.n_a, a.pos_base, enc_pos<SLOTS>(a, p1, s1), raw, warp,
+                      nthreads / 32, lane);
     cp_async_commit();
     issue_rows(t1, p1, s1, 1);
     cp_async_commit();
@@ -627,8 +662,9 @@ __global__ void __launch_bounds__(256, 2) encode_kernel(const CodecArgs a) {
     cp_async_commit();
   }
   if (my_tiles > 2) {
-    pp_pref = enc_pair(a, tile(2).p0, slot_l);
-    src_pref = enc_src(a, pp_pref);
+    pp_pref = enc_pair<SLOTS>(a, tile(2).p0, slot_l);
+    src_pref = enc_src<SLOTS>(a, pp_pref);
+    if (ROPE) pos_pref = enc_pos<SLOTS>(a, pp_pref, src_pref);
   }
 
   // Per iteration two groups are committed, [RoPE rows of k+2] then [rows of
@@ -640,7 +676,7 @@ __global__ void __launch_bounds__(256, 2) encode_kernel(const CodecArgs a) {
 
     const EncTile tl = tile(k);
     const int h = tl.group * a.hg + warp;
-    const EncPair ep = enc_pair(a, tl.p0, slot_l);
+    const EncPair ep = enc_pair<SLOTS>(a, tl.p0, slot_l);
     unsigned char* st = smem + s * stage_bytes;
     // lanes past the last pair run on whatever their staging row holds; none
     // of their results is stored
@@ -652,19 +688,20 @@ __global__ void __launch_bounds__(256, 2) encode_kernel(const CodecArgs a) {
                   nthreads);
     sync();  // stage s and the raw rows are free
     if (k + 2 < my_tiles) {
-      if (ROPE) issue_rope_rows(a.tab, a.n_a, a.pos_base, src_pref, raw, warp, nthreads / 32, lane);
+      if (ROPE) issue_rope_rows(a.tab, a.n_a, a.pos_base, pos_pref, raw, warp, nthreads / 32, lane);
       cp_async_commit();
       issue_rows(tile(k + 2), pp_pref, src_pref, s);
       cp_async_commit();
       if (k + 3 < my_tiles) {  // used next iteration
-        pp_pref = enc_pair(a, tile(k + 3).p0, slot_l);
-        src_pref = enc_src(a, pp_pref);
+        pp_pref = enc_pair<SLOTS>(a, tile(k + 3).p0, slot_l);
+        src_pref = enc_src<SLOTS>(a, pp_pref);
+        if (ROPE) pos_pref = enc_pos<SLOTS>(a, pp_pref, src_pref);
       }
     } else {
       cp_async_commit();
       cp_async_commit();
     }
-    const int64_t vec = ep.unit * a.pu + h * a.ph + a.slot0 + ep.slot;
+    const int64_t vec = enc_vec<SLOTS>(a, ep, h);
     void* meta = EXACT ? static_cast<void*>(reinterpret_cast<uint16_t*>(a.meta) + vec)
                        : static_cast<void*>(a.meta + vec);
     quantise_half<BITS, EXACT>(v, half, ep.valid, a.codes + vec * (4 * BITS), meta);
@@ -1434,7 +1471,7 @@ static cudaError_t launch_one(bool decode, CodecArgs a, int units, cudaStream_t 
     fn = reinterpret_cast<const void*>(decode_kernel<BITS, ROPE, EXACT>);
   } else {
     smem = 2 * (static_cast<size_t>(rows_bytes) + (ROPE ? kCsBytes : 0)) + (ROPE ? kRawBytes : 0);
-    fn = reinterpret_cast<const void*>(encode_kernel<BITS, ROPE, EXACT>);
+    fn = reinterpret_cast<const void*>(encode_kernel<BITS, ROPE, EXACT, false>);
   }
   cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
@@ -1451,7 +1488,7 @@ static cudaError_t launch_one(bool decode, CodecArgs a, int units, cudaStream_t 
   if (decode)
     decode_kernel<BITS, ROPE, EXACT><<<static_cast<unsigned>(grid), threads, smem, stream>>>(a, map);
   else
-    encode_kernel<BITS, ROPE, EXACT><<<static_cast<unsigned>(grid), threads, smem, stream>>>(a);
+    encode_kernel<BITS, ROPE, EXACT, false><<<static_cast<unsigned>(grid), threads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -1524,6 +1561,66 @@ cudaError_t launch_encode(const EncodeLaunch& L, cudaStream_t stream) {
     v.pu = L.v_out.unit_stride;
     v.ph = L.v_out.head_stride;
     return launch_kind(false, v, L.v_out.bits, false, L.exact, L.units, stream);
+  }
+  return cudaSuccess;
+}
+
+// One side (keys with RoPE, or values) of nq_encode_slots.
+template <int BITS, bool ROPE>
+static cudaError_t launch_slots(CodecArgs a, cudaStream_t stream) {
+  a.hg = pick_head_group(a.heads);
+  a.ngroups = a.heads / a.hg;
+  a.pairs = a.n;
+  a.num_tiles = (a.pairs + kSlots - 1) / kSlots * a.ngroups;
+  if (a.num_tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  a.div_groups = make_fastdiv(static_cast<uint32_t>(a.ngroups));
+  const int threads = 32 * a.hg;
+  const int smem = 2 * ((threads / 2) * kRowPad + (ROPE ? kCsBytes : 0)) + (ROPE ? kRawBytes : 0);
+  const void* fn = reinterpret_cast<const void*>(encode_kernel<BITS, ROPE, false, true>);
+  cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  int dev = 0, sms = 0, per_sm = 0;
+  if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
+  if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return err;
+  if ((err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, smem)) !=
+      cudaSuccess)
+    return err;
+  if (per_sm < 1) per_sm = 1;
+  const int64_t grid = min64(a.num_tiles, static_cast<int64_t>(sms) * per_sm);
+  encode_kernel<BITS, ROPE, false, true><<<static_cast<unsigned>(grid), threads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_encode_slots(const EncodeSlotsLaunch& L, cudaStream_t stream) {
+  CodecArgs a = common_args(L.heads, L.rows, 0, 0, L.positions, 0, L.rope_tab, L.rope_max_pos);
+  a.T_in = L.rows;
+  a.slots = L.slots;
+  a.div_page = make_fastdiv(static_cast<uint32_t>(L.page_size));
+  a.nslots = L.pages * L.page_size;
+  if (L.K) {
+    CodecArgs k = a;
+    k.kv = static_cast<const uint16_t*>(L.K);
+    k.sh = L.ks.head;
+    k.st = L.ks.token;
+    k.codes = L.k_out.codes;
+    k.meta = L.k_out.meta;
+    k.pu = L.k_out.unit_stride;
+    k.ph = L.k_out.head_stride;
+    const cudaError_t err = L.k_out.bits == 3 ? launch_slots<3, true>(k, stream)
+                                              : launch_slots<2, true>(k, stream);
+    if (err != cudaSuccess) return err;
+  }
+  if (L.V) {
+    CodecArgs v = a;
+    v.kv = static_cast<const uint16_t*>(L.V);
+    v.sh = L.vs.head;
+    v.st = L.vs.token;
+    v.codes = L.v_out.codes;
+    v.meta = L.v_out.meta;
+    v.pu = L.v_out.unit_stride;
+    v.ph = L.v_out.head_stride;
+    return L.v_out.bits == 3 ? launch_slots<3, false>(v, stream) : launch_slots<2, false>(v, stream);
   }
   return cudaSuccess;
 }

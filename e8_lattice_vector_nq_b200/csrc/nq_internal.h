@@ -67,8 +67,84 @@ struct AttendLaunch {
   void* ws;
 };
 
+struct EncodeSlotsLaunch {
+  const void* K;
+  nq_kv_strides ks;
+  const void* V;
+  nq_kv_strides vs;
+  int heads;
+  int64_t rows;
+  const int32_t* slots;
+  const int32_t* positions;
+  int page_size;
+  int64_t pages;
+  const float* rope_tab;
+  int64_t rope_max_pos;
+  nq_packed k_out, v_out;
+};
+
+struct PageTablesLaunch {
+  const int32_t *lens, *counts;
+  int requests, page_size;
+  const int32_t* free_pages;
+  int64_t n_free;
+  const int32_t* taken;
+  int32_t* table;
+  int64_t table_stride;
+  int32_t *lens_out, *starts, *slots, *positions;
+  int64_t max_rows;
+  int32_t* used;
+};
+
+struct NormRopeLaunch {
+  const void *q, *k;
+  nq_kv_strides qs, ks;
+  int q_heads, k_heads;
+  bool in_f32, q_f32, k_f32;
+  int units;
+  int64_t rows;
+  const float *q_weight, *k_weight;
+  float eps;
+  const int32_t* positions;
+  int64_t pos_stride, pos_base;
+  const float* rope_tab;
+  int64_t rope_max_pos;
+  void *q_out, *k_out;
+  nq_kv_strides qos, kos;
+};
+
+struct TreeLaunch {
+  const void *q, *K_new, *V_new;
+  nq_kv_strides qs, kns, vns;
+  int units, heads, G, nodes;
+  nq_packed k_in, v_in;
+  int64_t n;
+  const int32_t* lens;
+  const int32_t* table;
+  int64_t table_stride;
+  int page_size;
+  int64_t pages;
+  const int32_t* positions;
+  int64_t pos_stride, pos_base;
+  const float* rope_tab;
+  int64_t rope_max_pos;
+  const uint64_t* mask;
+  int64_t mask_stride;
+  float scale;
+  void* out;
+  nq_kv_strides os;
+  float* lse;
+  void* ws;
+};
+
 cudaError_t launch_encode(const EncodeLaunch& L, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeLaunch& L, cudaStream_t stream);
+cudaError_t launch_encode_slots(const EncodeSlotsLaunch& L, cudaStream_t stream);
+cudaError_t launch_page_tables(const PageTablesLaunch& L, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeLaunch& L, cudaStream_t stream);
+size_t tree_workspace_bytes(int units, int heads, int G, int nodes, int64_t n, bool shared);
+int64_t tree_ctas(int units, int heads, int G, int nodes, int64_t n);  // of its largest launch
+cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream);
 
 cudaError_t codec_read_clear_error(uint32_t* flags);
 // Decode engine (nq_decode_engine values), read at each decode launch.

@@ -53,6 +53,8 @@ EXPORTS = (
     "nq_entropy_workspace_bytes", "nq_entropy_encode", "nq_entropy_decode",
     "nq_packed_exact_bytes_per_vector", "nq_encode_exact", "nq_decode_exact",
     "nq_e8_box_quantise", "nq_set_decode_engine", "nq_get_decode_engine",
+    "nq_page_tables", "nq_qk_norm_rope", "nq_encode_slots", "nq_tree_attend",
+    "nq_tree_attend_workspace_bytes",
 )
 
 
@@ -100,6 +102,16 @@ def lib() -> ctypes.CDLL:
         "nq_decode_exact": (i32, [PX, PX, i32, i32, i64, i64, P, i64, i64, P, i64, P, KVStrides,
                                   P, KVStrides, P]),
         "nq_e8_box_quantise": (i32, [P, i64, i32, P, P, P]),
+        "nq_page_tables": (i32, [P, P, i32, i32, P, i64, P, P, i64, P, P, P, P, i64, P, P]),
+        "nq_qk_norm_rope": (i32, [P, KVStrides, i32, P, KVStrides, i32, i32, i32, i64, P, P,
+                                  ctypes.c_float, P, i64, i64, P, i64, P, KVStrides, i32, P,
+                                  KVStrides, i32, P]),
+        "nq_encode_slots": (i32, [P, KVStrides, P, KVStrides, i32, i64, P, P, i32, i64, P, i64,
+                                  PK, PK, P]),
+        "nq_tree_attend_workspace_bytes": (sz, [i32, i32, i32, i32, i64, i32]),
+        "nq_tree_attend": (i32, [P, KVStrides, P, KVStrides, P, KVStrides, i32, i32, i32, i32, PK,
+                                 PK, i64, P, P, i64, i32, i64, P, i64, i64, P, i64, P, i64,
+                                 ctypes.c_float, P, KVStrides, P, P, sz, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -516,6 +528,307 @@ def nq_entropy_decode(coded: EntropyCoded, out: PackedStore, slot0: int = 0, str
                                    ctypes.byref(d), int(slot0), _stream(stream)))
 
 
+# ------------------------------------------------------ serving a paged cache
+BF16, F32 = 0, 1
+_TYPES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+class _on:
+    """The device and the stream of a call, current while it runs: what the
+    call allocates then belongs to the stream that uses it."""
+
+    def __init__(self, device, stream):
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        if s.device != device:
+            raise ValueError(f"the stream is on {s.device}, the tensors are on {device}")
+        self.ctx = None
+        if torch.cuda.current_device() != device.index or stream is not None:
+            self.ctx = torch.cuda.stream(s)
+        self.ptr = ctypes.c_void_p(s.cuda_stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.ptr
+
+    def __exit__(self, *e):
+        if self.ctx is not None:
+            self.ctx.__exit__(*e)
+
+
+def _same_device(first: torch.Tensor, *ts) -> torch.device:
+    _require_cuda(first, *ts)
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return first.device
+
+
+def _int32(t: torch.Tensor, shape: tuple, name: str) -> None:
+    """An int32 tensor of that shape, its last dimension contiguous."""
+    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _positions(positions, units: int, n: int) -> int:
+    """Row stride of a positions list [units][>= n] (0: one row for all units)."""
+    if positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[0] != units:
+        raise ValueError(f"positions must be int32 [{units}, n]")
+    if positions.shape[1] < n or (n > 1 and positions.stride(1) != 1):
+        raise ValueError("positions must hold n contiguous entries per unit")
+    return positions.stride(0)
+
+
+def _strides4(t: torch.Tensor, types, name: str) -> KVStrides:
+    if t.dim() != 4 or t.shape[3] != D or t.stride(3) != 1 or t.dtype not in types:
+        raise ValueError(f"{name} must be [units, heads, rows, 128] with a contiguous last "
+                         f"dimension, of type {' or '.join(str(x) for x in types)}")
+    # a dimension of one index may carry any stride: give it one that is always valid
+    s = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
+    return KVStrides(*s)
+
+
+@dataclass
+class PageTables:
+    """Results of nq_page_tables (int32 device tensors; see nq.h): lens after
+    the call, starts [requests + 1], slots and positions [max_rows], used =
+    (pages taken, flags)."""
+
+    lens: torch.Tensor
+    starts: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    used: torch.Tensor
+
+    @classmethod
+    def empty(cls, requests: int, max_rows: int, device="cuda") -> "PageTables":
+        e = lambda n: torch.empty(n, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(e(requests), e(requests + 1), e(max_rows), e(max_rows), e(2))
+
+
+def nq_page_tables(lens: torch.Tensor, counts: torch.Tensor, page_size: int,
+                   free_pages: torch.Tensor, table: torch.Tensor, max_rows: int,
+                   taken: torch.Tensor | None = None, out: PageTables | None = None,
+                   stream=None) -> PageTables:
+    """Pages, slots and positions of counts[s] new tokens after lens[s] held
+    ones (see nq.h, nq_page_tables): fills the fresh entries of table
+    [requests][pages per request] in place from free_pages, whose first
+    taken[0] pages are gone already (none without taken)."""
+    dev = _same_device(lens, counts, free_pages, table, taken)
+    if taken is not None:
+        _int32(taken, (1,), "taken")
+    S = lens.shape[0]
+    _int32(lens, (S,), "lens")
+    _int32(counts, (S,), "counts")
+    _int32(free_pages, (free_pages.numel(),), "free_pages")
+    if table.dim() != 2 or table.shape[0] != S or table.dtype != torch.int32 or not table.is_contiguous():
+        raise ValueError(f"table must be a contiguous int32 [{S}, pages] tensor")
+    with _on(dev, stream) as st:
+        if out is None:
+            out = PageTables.empty(S, int(max_rows), dev)
+        else:
+            _same_device(lens, out.lens, out.starts, out.slots, out.positions, out.used)
+            _int32(out.lens, (S,), "out.lens")
+            _int32(out.starts, (S + 1,), "out.starts")
+            _int32(out.slots, (int(max_rows),), "out.slots")
+            _int32(out.positions, (int(max_rows),), "out.positions")
+            _int32(out.used, (2,), "out.used")
+        _check(lib().nq_page_tables(_ptr(lens), _ptr(counts), S, int(page_size), _ptr(free_pages),
+                                    free_pages.numel(), _ptr(taken), _ptr(table), max(table.shape[1], 1),
+                                    _ptr(out.lens), _ptr(out.starts), _ptr(out.slots),
+                                    _ptr(out.positions), int(max_rows), _ptr(out.used), st))
+    return out
+
+
+def nq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope_tab: torch.Tensor,
+                    rope_max_pos: int, positions: torch.Tensor | None = None, pos_base: int = 0,
+                    q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                    eps: float = 1e-6, q_dtype: torch.dtype | None = None,
+                    k_dtype: torch.dtype | None = None, q_out: torch.Tensor | None = None,
+                    k_out: torch.Tensor | None = None, stream=None):
+    """Per-head norm and RoPE of q [units][q_heads][rows][128] and k
+    [units][k_heads][rows][128] (bf16 or fp32, any strides that are multiples
+    of 8; see nq.h, nq_qk_norm_rope).  Returns (q_out, k_out), contiguous and
+    of the input's type unless q_out / k_out or q_dtype / k_dtype say
+    otherwise; q_out = q or k_out = k works in place."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q and k are both None")
+    dev = _same_device(ref, q, k, rope_tab, positions, q_weight, k_weight, q_out, k_out)
+    units, rows = ref.shape[0], ref.shape[2]
+    types = tuple(_TYPES)
+    for t, w, name in ((q, q_weight, "q"), (k, k_weight, "k")):
+        if t is not None and (t.dim() != 4 or t.shape[0] != units or t.shape[2] != rows
+                              or t.dtype != ref.dtype):
+            raise ValueError("q and k must share units, rows and type")
+        if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (D,) or w.stride(0) != 1):
+            raise ValueError(f"{name}_weight must be float32 [128]")
+    ps = _positions(positions, units, rows) if positions is not None else 0
+    with _on(dev, stream) as st:
+        args, outs = [], []
+        for t, o, dt, name in ((q, q_out, q_dtype, "q"), (k, k_out, k_dtype, "k")):
+            if t is None:
+                args.append((None, KVStrides(0, 0, 0), 0, None, KVStrides(0, 0, 0), BF16))
+                outs.append(None)
+                continue
+            s = _strides4(t, types, name)
+            if o is None:
+                o = torch.empty(t.shape, dtype=dt or t.dtype, device=dev)
+            elif tuple(o.shape) != tuple(t.shape) or (dt is not None and dt != o.dtype):
+                raise ValueError(f"{name}_out must have the shape of {name} and the type asked for")
+            os_ = _strides4(o, types, name + "_out")
+            args.append((_ptr(t), s, t.shape[1], _ptr(o), os_, _TYPES[o.dtype]))
+            outs.append(o)
+        (qp, qs, hq, qo, qos, qt), (kp, ks, hk, ko, kos, kt) = args
+        _check(lib().nq_qk_norm_rope(qp, qs, hq, kp, ks, hk, _TYPES[ref.dtype], units, rows,
+                                     _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions),
+                                     ps, int(pos_base), _ptr(rope_tab), int(rope_max_pos), qo, qos,
+                                     qt, ko, kos, kt, st))
+    return outs[0], outs[1]
+
+
+def nq_encode_slots(K: torch.Tensor | None, V: torch.Tensor | None, k_out: PackedStore | None,
+                    v_out: PackedStore | None, slots: torch.Tensor,
+                    positions: torch.Tensor | None = None, rope_tab: torch.Tensor | None = None,
+                    rope_max_pos: int = 0, stream=None):
+    """Encode row r of K, V [heads][rows][128] at position positions[r] into
+    slot slots[r] of paged stores [pages][heads][page_size] (see nq.h,
+    nq_encode_slots); rows with a slot outside the store are skipped."""
+    ref = K if K is not None else V
+    if ref is None:
+        raise ValueError("K and V are both None")
+    _require_device_readable(K, V)
+    stores = [s for t, s in ((K, k_out), (V, v_out)) if t is not None]
+    if any(s is None for s in stores):
+        raise ValueError("K needs k_out and V needs v_out")
+    dev = _same_device(slots, positions, rope_tab, *(t for s in stores for t in (s.codes, s.meta)),
+                       *(t for t in (K, V) if t is not None and t.is_cuda))
+    if ref.dim() != 3:
+        raise ValueError("K and V must be [heads, rows, 128]")
+    heads, rows = ref.shape[0], ref.shape[1]
+    _int32(slots, (rows,), "slots")
+    if K is not None and positions is None:
+        raise ValueError("keys need positions")
+    if positions is not None:
+        _int32(positions, (rows,), "positions")
+    pages, _, P = stores[0].meta.shape
+    for s in stores:
+        if tuple(s.meta.shape) != (pages, heads, P):
+            raise ValueError("the stores must be [pages][heads][page_size] alike")
+    view = lambda t: t[None] if t is not None else None  # noqa: E731
+    for t in (K, V):
+        if t is not None and tuple(t.shape) != (heads, rows, D):
+            raise ValueError("K and V must be [heads, rows, 128] alike")
+    if rows == 0:  # an empty tensor has no address
+        return
+    none = KVStrides(0, 0, 0)
+    kd = k_out.desc() if K is not None else None
+    vd = v_out.desc() if V is not None else None
+    with _on(dev, stream) as st:
+        _check(lib().nq_encode_slots(
+            _ptr(K), _strides4(view(K), (torch.bfloat16,), "K") if K is not None else none,
+            _ptr(V), _strides4(view(V), (torch.bfloat16,), "V") if V is not None else none,
+            heads, rows, _ptr(slots), _ptr(positions), P, pages, _ptr(rope_tab),
+            int(rope_max_pos), ctypes.byref(kd) if kd is not None else None,
+            ctypes.byref(vd) if vd is not None else None, st))
+
+
+def tree_attend_workspace(units: int, heads: int, G: int, nodes: int, n: int,
+                          shared: bool = True, device="cuda") -> torch.Tensor:
+    need = lib().nq_tree_attend_workspace_bytes(units, heads, G, nodes, int(n), int(shared))
+    return torch.empty(max(need, 16) // 4, dtype=torch.float32, device=device)
+
+
+def nq_tree_attend(q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
+                   k_in: PackedStore | None, v_in: PackedStore | None, n: int,
+                   rope_tab: torch.Tensor | None = None, rope_max_pos: int = 0,
+                   mask: torch.Tensor | None = None, lens: torch.Tensor | None = None,
+                   table: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                   pos_base: int = 0, scale: float | None = None,
+                   out: torch.Tensor | None = None, lse: bool = False,
+                   ws: torch.Tensor | None = None, stream=None):
+    """Attention of drafted nodes q [units][heads*G][nodes][128] over up to n
+    packed tokens per unit and over the nodes' own K_new, V_new
+    [units][heads][nodes][128] (all bf16; see nq.h, nq_tree_attend).
+
+    mask: int64 [units][nodes][ceil(nodes/64)] (or [nodes][...], shared), bit m
+    of a node's words = it sees node m; None = a chain.  lens: int32 [units]
+    tokens held (None: n for every unit).  table: int32 [units][pages per
+    unit], then k_in and v_in are [pages][heads][page_size].  Returns out like
+    q (bf16), or (out, lse fp32 [units][heads*G][nodes]) with lse=True."""
+    dev = _same_device(q, K_new, V_new, rope_tab, mask, lens, table, positions, out, ws,
+                       *(t for s in (k_in, v_in) if s is not None for t in (s.codes, s.meta)))
+    bf = (torch.bfloat16,)
+    qs, kns, vns = _strides4(q, bf, "q"), _strides4(K_new, bf, "K_new"), _strides4(V_new, bf, "V_new")
+    units, Hq, nodes, _ = q.shape
+    heads = K_new.shape[1]
+    if heads < 1 or Hq % heads:
+        raise ValueError("q has %d heads, not a multiple of the %d KV heads" % (Hq, heads))
+    if tuple(K_new.shape) != (units, heads, nodes, D) or tuple(V_new.shape) != tuple(K_new.shape):
+        raise ValueError("K_new and V_new must be [units, heads, nodes, 128]")
+    G, n = Hq // heads, int(n)
+    page, pages, tstride, ps, ms = 1, 0, 0, 0, 0
+    kd = vd = None
+    if n > 0:
+        if k_in is None or v_in is None or rope_tab is None:
+            raise ValueError("n > 0 needs k_in, v_in and rope_tab")
+        lead, h, cap = k_in.meta.shape
+        if tuple(v_in.meta.shape) != (lead, h, cap) or h != heads:
+            raise ValueError("k_in and v_in must be [units or pages][heads][slots] alike")
+        if table is None:
+            if lead < units or cap < n:
+                raise ValueError("packed store too small for units x n")
+        else:
+            if table.dim() != 2 or table.shape[0] != units or table.dtype != torch.int32:
+                raise ValueError(f"table must be int32 [{units}, pages]")
+            if table.shape[1] > 1 and table.stride(1) != 1:
+                raise ValueError("table must be contiguous in its last dimension")
+            page, pages = cap, lead
+            if table.shape[1] * page < n:
+                raise ValueError("a table row holds fewer than n tokens")
+            tstride = table.stride(0) if units > 1 else table.shape[1]
+            if units > 1 and tstride < table.shape[1]:
+                raise ValueError("table rows overlap")
+        if positions is not None:
+            ps = _positions(positions, units, n)
+            if units > 1 and ps < n:
+                raise ValueError("positions rows overlap")
+        kd, vd = k_in.desc(), v_in.desc()
+    if lens is not None:
+        _int32(lens, (units,), "lens")
+    if mask is not None:
+        words = (nodes + 63) // 64
+        if mask.dtype != torch.int64 or tuple(mask.shape) not in ((units, nodes, words), (nodes, words)):
+            raise ValueError(f"mask must be int64 [{units}, {nodes}, {words}] or [{nodes}, {words}]")
+        if not (mask if mask.dim() == 2 else mask[0] if units else mask).is_contiguous():
+            raise ValueError("mask rows must be contiguous")
+        ms = mask.stride(0) if mask.dim() == 3 and units > 1 else 0
+    L = lib()
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty(units, Hq, nodes, D, dtype=torch.bfloat16, device=dev)
+        elif tuple(out.shape) != tuple(q.shape):
+            raise ValueError("out must have the shape of q")
+        os_ = _strides4(out, bf, "out")
+        lse_t = torch.empty(units, Hq, nodes, dtype=torch.float32, device=dev) if lse else None
+        need = L.nq_tree_attend_workspace_bytes(units, heads, G, nodes, n, int(positions is None))
+        if ws is None:
+            ws = torch.empty(max(need, 16) // 4, dtype=torch.float32, device=dev)
+        elif not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
+        _check(L.nq_tree_attend(
+            _ptr(q), qs, _ptr(K_new), kns, _ptr(V_new), vns, units, heads, G, nodes,
+            ctypes.byref(kd) if kd is not None else None,
+            ctypes.byref(vd) if vd is not None else None, n, _ptr(lens),
+            _ptr(table) if n > 0 else None, tstride, page, pages,
+            _ptr(positions) if n > 0 else None, ps, int(pos_base), _ptr(rope_tab),
+            int(rope_max_pos), _ptr(mask), ms, float(scale if scale is not None else D ** -0.5),
+            _ptr(out), os_, _ptr(lse_t), _ptr(ws), ws.numel() * ws.element_size(), st))
+    return (out, lse_t) if lse else out
+
+
 DECODE_AUTO, DECODE_TENSOR_CORES, DECODE_CUDA_CORES = 0, 1, 2
 
 
@@ -756,3 +1069,59 @@ class AppendStore:
         """Slots 0..n-1 of `layer` for every sequence into [sequences][heads][n][128]."""
         nq_decode(self._units(self.k, layer=layer), self._units(self.v, layer=layer), n, K_out,
                   V_out, self.rope, self.cap, stream=stream)
+
+
+class PagedStore:
+    """Packed caches of many requests in shared pages: per layer a K and a V
+    store [pages][heads][page_size], one table of pages and one length per
+    request, all on the device.  A step of a server that drafts tokens:
+
+        out = store.attend(layer, q, K_new, V_new, mask)     # every layer
+        plan = store.plan(accepted_counts, max_rows)         # pages and slots
+        store.write(layer, K_rows, V_rows, plan.slots, plan.positions)
+        store.commit(plan)                                   # the new lengths
+
+    A prompt is the same with its own counts.  Tokens sit at their positions
+    (token t of a request at RoPE position t).  plan() changes nothing but
+    fresh table entries, so a plan may be dropped and made again."""
+
+    def __init__(self, requests: int, layers: int, heads: int, pages: int, page_size: int,
+                 max_tokens: int, theta: float, bits_k: int = 3, bits_v: int = 2, device="cuda"):
+        self.S, self.L, self.H, self.P, self.n = requests, layers, heads, page_size, max_tokens
+        self.rope = rope_tables(theta, max_tokens, device)
+        self.k = PackedStore.empty(layers * pages, heads, page_size, bits_k, device)
+        self.v = PackedStore.empty(layers * pages, heads, page_size, bits_v, device)
+        self.pages = pages
+        e = lambda *s, fill: torch.full(s, fill, dtype=torch.int32, device=device)  # noqa: E731
+        self.table = e(requests, (max_tokens + page_size - 1) // page_size, fill=-1)
+        self.lens, self.taken = e(requests, fill=0), e(1, fill=0)
+        self.free = torch.arange(pages, dtype=torch.int32, device=device)
+
+    def layer(self, layer: int) -> tuple[PackedStore, PackedStore]:
+        sl = slice(layer * self.pages, (layer + 1) * self.pages)
+        return self.k.select_units(sl), self.v.select_units(sl)
+
+    def plan(self, counts: torch.Tensor, max_rows: int, out: PageTables | None = None,
+             stream=None) -> PageTables:
+        """Pages, slots and positions for counts[s] more tokens of each request."""
+        return nq_page_tables(self.lens, counts, self.P, self.free, self.table, max_rows,
+                              taken=self.taken, out=out, stream=stream)
+
+    def write(self, layer: int, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor,
+              positions: torch.Tensor, stream=None):
+        """Encode K, V [heads][rows][128] into their slots (-1: skipped)."""
+        k, v = self.layer(layer)
+        nq_encode_slots(K, V, k, v, slots, positions, self.rope, self.n, stream=stream)
+
+    def commit(self, plan: PageTables):
+        """Take over the lengths and pages of a plan (on the current stream)."""
+        self.lens.copy_(plan.lens)
+        self.taken.copy_(plan.used[:1])
+
+    def attend(self, layer: int, q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
+               mask: torch.Tensor | None = None, n: int | None = None, **kw):
+        """Drafted nodes over the held tokens (at most n of each request, an
+        upper bound of the lengths known on the host) and over themselves."""
+        k, v = self.layer(layer)
+        return nq_tree_attend(q, K_new, V_new, k, v, self.n if n is None else n, self.rope, self.n,
+                              mask=mask, lens=self.lens, table=self.table, **kw)

@@ -369,6 +369,137 @@ nq_status nq_e8_quantise(const float *y, int64_t groups, int bits, uint32_t *cod
 nq_status nq_e8_box_quantise(const float *y, int64_t groups, int bits, uint32_t *codes,
                              uint8_t *coset, nq_stream_t stream);
 
+/* ---------------------------------------------------- page tables and slots
+ * Bookkeeping of a paged cache on the device, for a server whose batch lives
+ * there (request lengths never come back to the host, so a step can be
+ * captured in a graph).  A paged cache is a packed store whose units are
+ * PAGES of page_size slots; request s keeps its token t in slot t % page_size
+ * of page table[s*table_stride + t / page_size].
+ * Given the lengths lens[s] and the counts[s] new tokens of `requests`
+ * requests (int32; negative values count as 0):
+ *   have_s = ceil(lens_s / P), need_s = min(ceil((lens_s + counts_s) / P), table_stride),
+ *   fresh_s = max(need_s - have_s, 0), base_s = c + sum of fresh_r over r < s,
+ *                 c = taken ? max(*taken, 0) : 0 (pages already taken from the list),
+ *   table[s][j] = free_pages[base_s + j - have_s] for have_s <= j < need_s
+ *                 (-1 past the end of free_pages); other entries are not touched,
+ *   lens_out[s] = lens_s + counts_s (saturated at 2^31 - 1),
+ *   starts[s] = sum of counts_r over r < s, starts[requests] = their total
+ *                 (saturated at 2^31 - 1),
+ *   row starts[s] + i, 0 <= i < counts_s, is token t = lens_s + i:
+ *     slots[row] = table[s][t / P] * P + t % P, or -1 where the token has no
+ *                 page (an entry below 0, or past the table's row), or where
+ *                 that product does not fit 31 bits,
+ *     positions[row] = t,
+ *   rows from starts[requests] to max_rows - 1 (a padded batch): slot -1, position 0;
+ *   tokens past max_rows - 1 get no row,
+ *   used[0] = c + sum of fresh_s (pages then taken from the front of
+ *             free_pages: the next call's *taken; saturated at 2^31 - 1),
+ *   used[1] = bit 0: free_pages too short, bit 1: a token past its table row
+ *             or a request that starts in a page below 0, bit 2: more tokens than max_rows.
+ * The call changes none of lens, free_pages and *taken: repeated on the same
+ * values it gives the same tables.  slots, positions, lens_out, starts
+ * (int32 [requests + 1]) and used (int32 [2]) must not overlap lens, counts,
+ * free_pages, *taken or table.  1 <= requests <= 8192, 1 <= page_size <= 65536,
+ * 1 <= table_stride <= 2^24 (above: NQ_ERR_UNSUPPORTED); n_free >= 0,
+ * 0 <= max_rows < 2^31.  requests = 0 writes the rows and used only. */
+#define NQ_PAGE_TABLES_MAX_REQUESTS 8192
+nq_status nq_page_tables(const int32_t *lens, const int32_t *counts, int requests, int page_size,
+                         const int32_t *free_pages, int64_t n_free, const int32_t *taken,
+                         int32_t *table, int64_t table_stride, int32_t *lens_out, int32_t *starts, int32_t *slots,
+                         int32_t *positions, int64_t max_rows, int32_t *used,
+                         nq_stream_t stream);
+
+/* ------------------------------------- norms of queries and keys with RoPE
+ * The step before the cache: root-mean-square norm of every query and key
+ * head, then the rotary embedding at the row's position, in one pass:
+ *   y = x * rsqrt(sum(x^2) / 128 + eps) * w     (w = 1 where the weight is NULL)
+ *   o_i = fmaf(y_i, c, -(y_{i+64} s)),  o_{i+64} = fmaf(y_{i+64}, c, y_i s)
+ * at pos = pos_base + (positions ? positions[u*pos_stride + t] : t), (c, s)
+ * from rope_tab (fp32 throughout, one rounding to the output type).
+ * q: [units][q_heads][rows][128], k: [units][k_heads][rows][128], each of
+ * type in_type with its own strides (in elements of its own type; any order
+ * of the dimensions, views of one fused projection included; multiples of 8,
+ * bases 16-byte aligned).  q may be NULL with q_heads = 0, and so may k.
+ * q_out (q_type) and k_out (k_type) have the shapes of q and k; an output may
+ * be its own input (same pointer, strides and type), and must not overlap the
+ * inputs otherwise.  Types: NQ_BF16, NQ_F32.  q_weight, k_weight: fp32 [128]
+ * device arrays, 16-byte aligned.  eps >= 0 finite.  A list of positions must
+ * stay below rope_max_pos; out-of-contract entries read a row of the table
+ * all the same (no fault).  units * rows * heads < 2^31. */
+typedef enum { NQ_BF16 = 0, NQ_F32 = 1 } nq_dtype;
+nq_status nq_qk_norm_rope(const void *q, nq_kv_strides qs, int q_heads, const void *k,
+                          nq_kv_strides ks, int k_heads, int in_type, int units, int64_t rows,
+                          const float *q_weight, const float *k_weight, float eps,
+                          const int32_t *positions, int64_t pos_stride, int64_t pos_base,
+                          const float *rope_tab, int64_t rope_max_pos, void *q_out,
+                          nq_kv_strides qos, int q_type, void *k_out, nq_kv_strides kos,
+                          int k_type, nq_stream_t stream);
+
+/* ------------------------------------------------- encode into given slots
+ * nq_encode for rows that go anywhere: row r (0 <= r < rows) of every head is
+ * a token at RoPE position positions[r], coded exactly as nq_encode codes it,
+ * and written to slot slots[r] of a paged store, i.e. to vector
+ *   (slots[r] / page_size)*unit_stride + h*head_stride + slots[r] % page_size.
+ * Rows whose slot is outside [0, pages*page_size) (-1: a padded row, a
+ * rejected token) are skipped: nothing of them is written.  A contiguous
+ * cache of `units` sequences with cap slots is page_size = cap, pages = units.
+ * The slots of one call are distinct (as nq_page_tables gives them): rows
+ * that share a slot leave that vector unspecified (no fault).
+ * K, V: bf16 [heads][rows][128] with strides ks, vs (their unit is not read);
+ * either may be NULL; device or pinned host memory as for nq_encode.  slots,
+ * positions: int32 [rows] (positions is not read without K).  rows * heads
+ * and pages * page_size below 2^31. */
+nq_status nq_encode_slots(const void *K, nq_kv_strides ks, const void *V, nq_kv_strides vs,
+                          int heads, int64_t rows, const int32_t *slots,
+                          const int32_t *positions, int page_size, int64_t pages,
+                          const float *rope_tab, int64_t rope_max_pos, const nq_packed *k_out,
+                          const nq_packed *v_out, nq_stream_t stream);
+
+/* ------------------------------------------------ attention of a drafted tree
+ * nq_attend for several new tokens at once: `nodes` drafted tokens per unit
+ * attend to the unit's packed tokens and to each other along a tree.  For
+ * unit u, node i, query head j (KV head h = j / G), with one softmax over
+ *   - the packed tokens t < len_u, len_u = lens ? min(max(lens[u], 0), n) : n,
+ *       s = scale * dot(q[u][j][i], k_t),
+ *     k_t and v_t as for nq_attend (position pos_base + (positions ?
+ *     positions[u*pos_stride + t] : t)), in slot t of unit u, or, with a page
+ *     table, in slot t % page_size of page table[u*table_stride + t /
+ *     page_size] (nq_page_tables); a token whose page is outside [0, pages)
+ *     is left out;
+ *   - the draft nodes m that node i sees: bit m % 64 of word
+ *     mask[u*mask_stride + i*ceil(nodes/64) + m/64]; without a mask, m <= i
+ *     (a chain).  s = scale * dot(q[u][j][i], K_new[u][h][m]), value
+ *     V_new[u][h][m].  mask_stride 0 shares one mask among the units.
+ *   out[u][j][i] = sum softmax(s) v (bf16), lse[(u*heads*G + j)*nodes + i] =
+ *   log sum exp(s) (fp32, may be NULL).  A row that sees nothing gives 0 and
+ *   -infinity.
+ * q: bf16 [units][heads*G][nodes][128] (strides qs); K_new, V_new: bf16
+ * [units][heads][nodes][128], already rotated (nq_qk_norm_rope); out like q
+ * (strides os; must not overlap the inputs).  The packed part runs on the
+ * tensor cores with f16 operands and fp32 accumulators: keys are rounded to
+ * f16 after the rotation (2^-12 relative, as are the cos/sin), queries are
+ * scaled by a power of two per row (exact), softmax weights and fp16-scaled
+ * codes are rounded to f16, and statistics, sums and the draft part are fp32.
+ * Queries must be finite with |q| <= 2^100, draft keys and values finite.
+ * Scores beyond 2^15 (in log2 units) are out of range of the fp32 exponent
+ * arithmetic's precision, as for any fp32 softmax.
+ * 1 <= G <= 8, 0 <= n < 2^31 (n = 0: the draft alone, k_in and v_in are not
+ * read), 1 <= nodes <= 1024.  ws: nq_tree_attend_workspace_bytes(units,
+ * heads, G, nodes, n, shared) bytes, 16-byte aligned, shared = 1 when
+ * positions is NULL (one table of angles for all units), else 0. */
+#define NQ_TREE_MAX_NODES 1024
+size_t nq_tree_attend_workspace_bytes(int units, int heads, int G, int nodes, int64_t n,
+                                      int shared);
+nq_status nq_tree_attend(const void *q, nq_kv_strides qs, const void *K_new, nq_kv_strides kns,
+                         const void *V_new, nq_kv_strides vns, int units, int heads, int G,
+                         int nodes, const nq_packed *k_in, const nq_packed *v_in, int64_t n,
+                         const int32_t *lens, const int32_t *table, int64_t table_stride,
+                         int page_size, int64_t pages, const int32_t *positions,
+                         int64_t pos_stride, int64_t pos_base, const float *rope_tab,
+                         int64_t rope_max_pos, const uint64_t *mask, int64_t mask_stride,
+                         float scale, void *out, nq_kv_strides os, float *lse, void *ws,
+                         size_t ws_bytes, nq_stream_t stream);
+
 /* ------------------------------------------------------- decode engine
  * Which kernel nq_decode / nq_decode_exact run (process-wide, default
  * NQ_DECODE_AUTO):

@@ -1,0 +1,175 @@
+"""Argument checks of the serving calls (page tables, norms with RoPE, encode
+into slots, tree attention), on the CPU: every refused call returns its status
+before anything is launched (the pointers are never dereferenced), empty work
+is accepted without a device, and host tensors are refused by the binding."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def nq():
+    from e8_lattice_vector_nq_b200 import build, nq as nqmod
+
+    build.build()
+    return nqmod
+
+
+def ptr(x):
+    return ctypes.c_void_p(x)
+
+
+A, B, C, E, F, G, H = (0x10000000 * i for i in range(1, 8))  # far apart, 16-byte aligned
+
+
+def pages(nq, **kw):
+    a = dict(lens=A, counts=B, requests=4, page=16, free=C, n_free=100, taken=None, table=E,
+             stride=8, lens_out=F, starts=G, slots=H, positions=H + 0x1000000, rows=64,
+             used=H + 0x2000000)
+    a.update(kw)
+    p = lambda k: None if a[k] is None else ptr(a[k])  # noqa: E731
+    return nq.lib().nq_page_tables(p("lens"), p("counts"), a["requests"], a["page"], p("free"),
+                                   a["n_free"], p("taken"), p("table"), a["stride"],
+                                   p("lens_out"), p("starts"), p("slots"), p("positions"),
+                                   a["rows"], p("used"), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(requests=-1), 1), (dict(page=0), 1), (dict(stride=0), 1), (dict(n_free=-1), 1),
+    (dict(rows=-1), 1), (dict(requests=8193), 4), (dict(page=65537), 4), (dict(rows=1 << 31), 4),
+    (dict(stride=(1 << 24) + 1), 4), (dict(lens=None), 1), (dict(table=None), 1),
+    (dict(starts=None), 1), (dict(used=None), 1), (dict(free=None), 1), (dict(slots=None), 1),
+    (dict(slots=H + 2), 1), (dict(taken=C + 1), 1),
+    # in-place lengths, slots over the free list, a cursor inside used, tables over lens
+    (dict(lens_out=A), 1), (dict(slots=C + 16), 1), (dict(taken=H + 0x2000000), 1),
+    (dict(table=A - 64), 1), (dict(positions=H + 128), 1),
+])
+def test_page_tables_refusals(nq, kw, status):
+    assert pages(nq, **kw) == status, nq.lib().nq_last_error()
+
+
+def norm(nq, **kw):
+    S = nq.KVStrides
+    a = dict(q=A, qs=S(0, 128, 4096), qh=32, k=B, ks=S(0, 128, 1024), kh=8, t=0, units=1, rows=4,
+             wq=None, wk=None, eps=1e-6, pos=None, pstride=0, base=0, tab=C, maxp=64, qo=E,
+             qos=S(0, 128, 4096), qt=0, ko=F, kos=S(0, 128, 1024), kt=0)
+    a.update(kw)
+    p = lambda k: None if a[k] is None else ptr(a[k])  # noqa: E731
+    return nq.lib().nq_qk_norm_rope(p("q"), a["qs"], a["qh"], p("k"), a["ks"], a["kh"], a["t"],
+                                    a["units"], a["rows"], p("wq"), p("wk"), a["eps"], p("pos"),
+                                    a["pstride"], a["base"], p("tab"), a["maxp"], p("qo"),
+                                    a["qos"], a["qt"], p("ko"), a["kos"], a["kt"], None)
+
+
+def test_norm_rope_refusals(nq):
+    S = nq.KVStrides
+    inv, uns = nq.NQ_ERR_INVALID, nq.NQ_ERR_UNSUPPORTED
+    assert norm(nq, qh=0, kh=0) == inv
+    assert norm(nq, qh=1025) == inv and norm(nq, rows=-1) == inv and norm(nq, base=-1) == inv
+    assert norm(nq, eps=-1.0) == inv and norm(nq, eps=float("nan")) == inv
+    assert norm(nq, eps=float("inf")) == inv
+    assert norm(nq, t=2) == inv and norm(nq, qt=-1) == inv and norm(nq, kt=3) == inv
+    assert norm(nq, q=None) == inv and norm(nq, ko=None) == inv and norm(nq, q=A + 8) == inv
+    assert norm(nq, qs=S(0, 128, 4100)) == inv and norm(nq, qs=S(0, -128, 4096)) == inv
+    # outputs that several rows would write
+    assert norm(nq, qos=S(0, 0, 4096)) == inv and norm(nq, qos=S(0, 128, 0)) == inv
+    assert norm(nq, units=2) == inv
+    # in place only as it is
+    assert norm(nq, qo=A, qos=S(0, 512, 128)) == inv and norm(nq, qo=A, qt=1) == inv
+    assert norm(nq, wq=C + 4) == inv
+    assert norm(nq, tab=None) == inv and norm(nq, base=61) == inv and norm(nq, maxp=0) == inv
+    assert norm(nq, units=2, pos=F, pstride=3, qos=S(1 << 20, 128, 4096),
+                kos=S(1 << 20, 128, 1024)) == inv
+    assert norm(nq, rows=1 << 30, maxp=1 << 31) == uns
+    assert norm(nq, units=0) == 0 and norm(nq, rows=0) == 0
+
+
+def slots(nq, **kw):
+    S = nq.KVStrides
+    pk = nq.Packed(0x20000, 0x30000, 64, 8, 3)
+    a = dict(K=A, ks=S(0, 128, 1024), V=B, vs=S(0, 128, 1024), heads=8, rows=4, slots=C,
+             positions=E, page=8, pages=4, tab=F, maxp=64, kout=pk, vout=pk)
+    a.update(kw)
+    p = lambda k: None if a[k] is None else ptr(a[k])  # noqa: E731
+    d = lambda k: None if a[k] is None else ctypes.byref(a[k])  # noqa: E731
+    return nq.lib().nq_encode_slots(p("K"), a["ks"], p("V"), a["vs"], a["heads"], a["rows"],
+                                    p("slots"), p("positions"), a["page"], a["pages"], p("tab"),
+                                    a["maxp"], d("kout"), d("vout"), None)
+
+
+def test_encode_slots_refusals(nq):
+    S = nq.KVStrides
+    inv, uns = nq.NQ_ERR_INVALID, nq.NQ_ERR_UNSUPPORTED
+    assert slots(nq, K=None, V=None) == inv
+    for kw in (dict(heads=0), dict(rows=-1), dict(page=0), dict(pages=-1), dict(slots=None),
+               dict(slots=C + 2), dict(positions=None), dict(tab=None), dict(maxp=0),
+               dict(kout=None), dict(vout=None, K=None),
+               dict(kout=nq.Packed(0x20000, 0x30000, 64, 8, 4)), dict(ks=S(0, 128, 1020)),
+               dict(K=A + 2)):
+        assert slots(nq, **kw) == inv, kw
+    assert slots(nq, rows=1 << 29) == uns and slots(nq, pages=1 << 29) == uns
+    assert slots(nq, rows=0) == 0
+
+
+def tree(nq, **kw):
+    S = nq.KVStrides
+    pk = nq.Packed(0x20000, 0x30000, 4096, 512, 3)
+    a = dict(q=A, qs=S(1 << 16, 128, 4096), K=B, ks=S(1 << 14, 128, 1024), V=C,
+             vs=S(1 << 14, 128, 1024), units=2, heads=8, G=4, nodes=5, kin=pk, vin=pk, n=100,
+             lens=None, table=None, tstride=0, page=1, pages=0, pos=None, pstride=0, base=0,
+             tab=E, maxp=100, mask=None, mstride=0, scale=0.1, out=F, os=S(1 << 16, 128, 4096),
+             lse=None, ws=G, wsb=1 << 40)
+    a.update(kw)
+    p = lambda k: None if a[k] is None else ptr(a[k])  # noqa: E731
+    d = lambda k: None if a[k] is None else ctypes.byref(a[k])  # noqa: E731
+    return nq.lib().nq_tree_attend(
+        p("q"), a["qs"], p("K"), a["ks"], p("V"), a["vs"], a["units"], a["heads"], a["G"],
+        a["nodes"], d("kin"), d("vin"), a["n"], p("lens"), p("table"), a["tstride"], a["page"],
+        a["pages"], p("pos"), a["pstride"], a["base"], p("tab"), a["maxp"], p("mask"),
+        a["mstride"], a["scale"], p("out"), a["os"], p("lse"), p("ws"), a["wsb"], None)
+
+
+def test_tree_attend_refusals(nq):
+    S = nq.KVStrides
+    inv, uns = nq.NQ_ERR_INVALID, nq.NQ_ERR_UNSUPPORTED
+    for kw in (dict(units=-1), dict(heads=0), dict(G=0), dict(G=9), dict(nodes=0),
+               dict(nodes=1025), dict(n=-1), dict(base=-1), dict(scale=float("nan")),
+               dict(q=None), dict(K=None), dict(V=None), dict(out=None), dict(q=A + 2),
+               dict(qs=S(1 << 16, 128, 4097)), dict(os=S(0, 128, 4096)), dict(os=S(1 << 16, 0, 4096)),
+               dict(out=A), dict(out=B), dict(lse=F + 2), dict(lens=F + 1), dict(mask=F + 4),
+               dict(mask=F, mstride=4), dict(kin=None), dict(vin=None), dict(tab=None),
+               dict(kin=nq.Packed(0x20000, 0x30000, 64, 8, 1)), dict(maxp=99), dict(base=1),
+               dict(pos=F, pstride=99), dict(table=F, tstride=6, page=16), dict(table=F, page=0),
+               dict(table=F, tstride=7, page=16, pages=-1), dict(table=F + 2, tstride=7, page=16),
+               dict(ws=None), dict(ws=G + 8)):
+        assert tree(nq, **kw) == inv, kw
+    assert tree(nq, wsb=16) == nq.NQ_ERR_WORKSPACE
+    assert tree(nq, n=1 << 31, maxp=1 << 32) == uns
+    assert tree(nq, units=1 << 20, nodes=1024) == uns
+    assert tree(nq, units=0) == 0
+
+
+def test_tree_workspace_sizes(nq):
+    L = nq.lib()
+    assert L.nq_tree_attend_workspace_bytes(1, 8, 4, 1, 0, 1) == 0
+    assert L.nq_tree_attend_workspace_bytes(0, 8, 4, 1, 100, 1) == 0
+    small = L.nq_tree_attend_workspace_bytes(1, 8, 4, 1, 100, 1)
+    assert 0 < small < L.nq_tree_attend_workspace_bytes(1, 8, 4, 64, 100, 1)
+    assert small <= L.nq_tree_attend_workspace_bytes(1, 8, 4, 1, 100000, 1)
+
+
+def test_binding_refuses_host_tensors(nq):
+    bf = torch.zeros(1, 8, 4, 128, dtype=torch.bfloat16)
+    i = torch.zeros(4, dtype=torch.int32)
+    st = nq.PackedStore.empty(4, 8, 16, 3, "cpu")
+    tab = torch.zeros(16)
+    calls = {
+        "page_tables": lambda: nq.nq_page_tables(i, i, 16, i, i.view(4, 1), 8),
+        "norm_rope": lambda: nq.nq_qk_norm_rope(bf, bf, tab, 64),
+        "encode_slots": lambda: nq.nq_encode_slots(bf[0], bf[0], st, st, i, i, tab, 64),
+        "tree_attend": lambda: nq.nq_tree_attend(bf, bf, bf, st, st, 16, tab, 64),
+    }
+    for name, call in calls.items():
+        with pytest.raises(ValueError, match="no CPU path"):
+            call()

@@ -823,7 +823,11 @@ int nq_get_decode_engine(void) { return nq::decode_engine(); }
 
 nq_status nq_device_error(uint32_t* flags_out) {
   if (!flags_out) return fail(NQ_ERR_INVALID, "flags_out is NULL");
-  return cuda_status(nq::codec_read_clear_error(flags_out), "nq_device_error");
+  uint32_t codec = 0, tree = 0;
+  cudaError_t err = nq::codec_read_clear_error(&codec);
+  if (err == cudaSuccess) err = nq::tree_read_clear_error(&tree);
+  if (err == cudaSuccess) *flags_out = codec | tree;
+  return cuda_status(err, "nq_device_error");
 }
 
 }  // extern "C"

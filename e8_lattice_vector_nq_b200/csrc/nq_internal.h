@@ -144,6 +144,7 @@ cudaError_t launch_page_tables(const PageTablesLaunch& L, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeLaunch& L, cudaStream_t stream);
 size_t tree_workspace_bytes(int units, int heads, int G, int nodes, int64_t n, bool shared);
 int64_t tree_ctas(int units, int heads, int G, int nodes, int64_t n);  // of its largest launch
+cudaError_t tree_read_clear_error(uint32_t* flags);  // after a synchronisation
 cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream);
 
 cudaError_t codec_read_clear_error(uint32_t* flags);

@@ -1,21 +1,71 @@
 // nq_tree.cu -- attention of a tree of drafted tokens over the packed cache
 // (sm_100a).  Formulas: include/nq.h, nq_tree_attend.
+//
+// The R = nodes * G query rows of one KV head share the head's tokens, so a
+// token is unpacked once for all of them and the two products run on the
+// tensor cores with the TOKENS as the 128 rows of the MMA and the query rows
+// as its N columns (N = 16 .. 128 as the call needs, so a single new token
+// does not pay for 128 rows).  Per tile of 128 tokens and one KV head:
+//   1. keys: codes -> t = 2q (f16 integers, exact); X = t H on the tensor
+//      cores: with H128 = [[H64, H64], [H64, -H64]] the two halves u = H64 t_lo
+//      and v = H64 t_hi take half the products, and the last butterfly costs
+//      nothing inside the rotation:
+//        o_i = u c' + v s',  o_{i+64} = u s' - v c',  c' = c - s, s' = c + s.
+//      o is rounded to f16 (|o| < 1268: no scale is applied before the product,
+//      so no scale can overflow it) and the key's scale kappa_t multiplies the
+//      score, where a thread has one token and kappa_t is its scalar;
+//   2. S^T = o Q^T (fp32 in TMEM), Q scaled per row by a power of two;
+//   3. y = S f_r kappa_t - m_r in log2 units, p = 2^y; the sum over tokens is
+//      kept per thread and reduced once at the end;
+//   4. O^T += V' P, V' = 2^(e-2) t and P = f16(p m) for the value's scale sigma
+//      = 2^e m, so V' is exact and a token's weight is rounded once (no
+//      transform: the codes' coordinates are summed, and H is applied once per
+//      row at the end).
+// m_r is not the running maximum but a reference kept within 2^8 of it: p
+// starts at 2^6 and stays below 2^14, so the maximum may grow by 2^8 before
+// the sums are rescaled, and f16 holds p down to 2^-30 of the maximum.  A tile whose
+// scores leave that range (the first one always) takes the exact column
+// maxima; the others only compare (one vote per tile and warpgroup).
+//
+// One CTA per SM: four warpgroups of compute threads (thread: one token of
+// the tile; warpgroup: a quarter of the coordinates in 1 and 4, of the query
+// rows in 3), one warp that issues every MMA, one that stages codes
+// (cp.async, three tiles ahead, page by page).  The MMAs of a step run while
+// the threads work on the next: T(j+1) | softmax(j) | rotate(j+1) | V(j+1)
+// against S(j) | X(j+1) | O(j) | S(j+1).  The work of a launch is split over
+// the tokens (flash decoding) to fill the 148 SMs; tree_combine_kernel merges
+// the splits, applies H and attends the draft nodes in fp32.
+//
+// The angles of a tile are needed by every KV head and every row block:
+// tree_angles_kernel writes (c', s') once per call as f16 pairs in the order
+// in which the compute threads read them.
 #include "nq_codec_math.cuh"
 #include "nq_internal.h"
+#include "nq_tcgen05.cuh"
 
 namespace nq {
 
-constexpr int kTreeTile = 128;            // tokens per tile
-constexpr int kTreePart = 2 + kD;         // a split's m (log2 units), l, sums[128]
-constexpr int kTreePitch = kD + 4;        // floats per staged row
+constexpr int kTreeTile = 128;     // tokens per tile
+constexpr int kTreePart = 2 + kD;  // a split's m (log2 units), l, sums[128] in the code domain
+constexpr int kTreeStages = 3;
+constexpr int kTreeThreads = 512 + 64;  // compute threads, issuing warp, staging warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kTreeWaitLimit = 1u << 20;
+constexpr uint32_t kErrTreeTimeout = 4u;
 
 struct TreeArgs {
   TreeLaunch L;
-  int rows;  // nodes * G rows per KV head, row = node * G + g
-  int64_t n_a, chunk, nsplit;
-  float* part;  // [units * heads][rows][nsplit][kTreePart]
+  int rows;         // nodes * G rows per KV head, row = node * G + g
+  int ncols;        // query rows per CTA (4 * NR)
+  int rblocks;      // CTAs per (unit, KV head, split)
+  int64_t n_a;
+  int64_t tiles;    // ceil(n / 128)
+  int64_t per;      // tiles per split
+  int64_t nsplit;
+  float* part;      // [units * heads][rows][nsplit][kTreePart]
+  uint4* angles;    // [units or 1][tiles][4][4][128]
+  int64_t angle_stride;  // entries per unit, 0 when shared
 };
 
 __device__ __forceinline__ int64_t tree_len(const TreeLaunch& L, int64_t u) {
@@ -24,131 +74,705 @@ __device__ __forceinline__ int64_t tree_len(const TreeLaunch& L, int64_t u) {
   return v < 0 ? 0 : (v > L.n ? L.n : v);
 }
 
-// Vector index of token t of unit u, head h; -1 when its page is out of range.
-__device__ __forceinline__ int64_t tree_vec(const TreeLaunch& L, const nq_packed& p, int64_t u,
-                                            int h, int64_t t) {
-  if (!L.table) return u * p.unit_stride + h * p.head_stride + t;
-  const uint32_t j = static_cast<uint32_t>(t) / static_cast<uint32_t>(L.page_size);
-  const int64_t page = __ldg(L.table + u * L.table_stride + j);
-  if (page < 0 || page >= L.pages) return -1;
-  return page * p.unit_stride + h * p.head_stride + (t - static_cast<int64_t>(j) * L.page_size);
-}
-
-template <int BITS>
-__device__ __forceinline__ void tree_codes(const nq_packed& p, int64_t vec,
-                                           uint32_t (&w)[4 * BITS], uint32_t& meta) {
+// ------------------------------------------------------------------ angles
+// Thread (t, w) of a tile: c' = c - s and s' = c + s of its token at the
+// frequencies 16w .. 16w+15, entry x holding frequencies 16w+4x .. +3 as
+// (c' pair, s' pair, c' pair, s' pair).
+__global__ void __launch_bounds__(512) tree_angles_kernel(const TreeArgs a) {
+  const int t = threadIdx.x & 127, w = threadIdx.x >> 7;
+  const int64_t tile = blockIdx.x % a.tiles, u = blockIdx.x / a.tiles;
+  const int64_t tok = tile * kTreeTile + t;
+  int64_t pos = 0;
+  if (tok < a.L.n) {
+    const int32_t p = a.L.positions ? __ldg(a.L.positions + u * a.L.pos_stride + tok)
+                                    : static_cast<int32_t>(tok);
+    pos = a.L.pos_base + (p < 0 ? 0 : p);  // out-of-contract positions stay in bounds
+  }
+  int64_t hi = pos >> 8;
+  hi = hi >= a.n_a ? a.n_a - 1 : hi;
+  const float4* ra = reinterpret_cast<const float4*>(a.L.rope_tab) + hi * (kHalf / 2) + 8 * w;
+  const float4* rb =
+      reinterpret_cast<const float4*>(a.L.rope_tab) + (a.n_a + (pos & 255)) * (kHalf / 2) + 8 * w;
+  uint4* out = a.angles + u * a.angle_stride + ((tile * 4 + w) * 4) * 128 + t;
 #pragma unroll
-  for (int c = 0; c < 4 * BITS; ++c) w[c] = vec < 0 ? 0u : __ldg(p.codes + vec * (4 * BITS) + c);
-  meta = vec < 0 ? 0u : __ldg(p.meta + vec);
-}
-
-template <int BK, int BV>
-__global__ void __launch_bounds__(256, 1) tree_partial_kernel(const TreeArgs a) {
-  extern __shared__ __align__(16) float tree_smem[];
-  float* ks = tree_smem;
-  float* vs = ks + kTreeTile * kTreePitch;
-  float* qs = vs + kTreeTile * kTreePitch;  // [8 warps][128]
-  float* ps = qs + 8 * kD;                  // [8 warps][128]
-  const TreeLaunch& L = a.L;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slot_l = lane & 15, half = lane >> 4;
-  const int64_t split = blockIdx.x % a.nsplit, uh = blockIdx.x / a.nsplit;
-  const int64_t u = uh / L.heads;
-  const int h = static_cast<int>(uh % L.heads);
-  const int64_t len = tree_len(L, u);
-  const int64_t t0 = split * a.chunk, t1 = min64(t0 + a.chunk, len);
-  const float2* tab = reinterpret_cast<const float2*>(L.rope_tab);
-
-  for (int64_t tile = t0; tile < t1 || tile == t0; tile += kTreeTile) {
-    __syncthreads();
-    const int tok = warp * kSlots + slot_l;
-    const int64_t t = tile + tok;
-    {
-      const bool in = t < t1;
-      uint32_t wk[4 * BK], wv[4 * BV], mk, mv;
-      const int64_t vk = in ? tree_vec(L, L.k_in, u, h, t) : -1;
-      const int64_t vv = in ? tree_vec(L, L.v_in, u, h, t) : -1;
-      tree_codes<BK>(L.k_in, vk, wk, mk);
-      tree_codes<BV>(L.v_in, vv, wv, mv);
-      float2 v[32];
-      reconstruct_half<BK>(wk, mk, half, v);
-      int64_t pos = 0;
-      if (in) {
-        int32_t p = L.positions ? __ldg(L.positions + u * L.pos_stride + t) : static_cast<int32_t>(t);
-        pos = L.pos_base + (p < 0 ? 0 : p);
-      }
-      int64_t hi = pos >> 8;
-      hi = hi >= a.n_a ? a.n_a - 1 : hi;
-      const float2* ra = tab + hi * kHalf + 32 * half;
-      const float2* rb = tab + (a.n_a + (pos & 255)) * kHalf + 32 * half;
+  for (int x = 0; x < 4; ++x) {
+    uint32_t e[4];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float2 A = __ldg(ra + j), B = __ldg(rb + j);
-        const float c = __fmaf_rn(A.x, B.x, -__fmul_rn(A.y, B.y));
-        const float s = __fmaf_rn(A.y, B.x, __fmul_rn(A.x, B.y));
-        const float x = v[j].x, y = v[j].y;
-        ks[tok * kTreePitch + 32 * half + j] = __fmaf_rn(x, c, -__fmul_rn(y, s));
-        ks[tok * kTreePitch + 64 + 32 * half + j] = __fmaf_rn(y, c, __fmul_rn(x, s));
-      }
-      reconstruct_half<BV>(wv, mv, half, v);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        vs[tok * kTreePitch + 32 * half + j] = v[j].x;
-        vs[tok * kTreePitch + 64 + 32 * half + j] = v[j].y;
-      }
+    for (int y = 0; y < 2; ++y) {
+      const float4 A = __ldg(ra + 2 * x + y), B = __ldg(rb + 2 * x + y);
+      const float c0 = __fmaf_rn(A.x, B.x, -__fmul_rn(A.y, B.y));
+      const float s0 = __fmaf_rn(A.y, B.x, __fmul_rn(A.x, B.y));
+      const float c1 = __fmaf_rn(A.z, B.z, -__fmul_rn(A.w, B.w));
+      const float s1 = __fmaf_rn(A.w, B.z, __fmul_rn(A.z, B.w));
+      const __half2 cc = __floats2half2_rn(c0 - s0, c1 - s1);
+      const __half2 ss = __floats2half2_rn(c0 + s0, c1 + s1);
+      e[2 * y] = *reinterpret_cast<const uint32_t*>(&cc);
+      e[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&ss);
     }
-    __syncthreads();
-    float* q = qs + warp * kD;
-    float* p = ps + warp * kD;
-    for (int r = warp; r < a.rows; r += 8) {
-      const int node = r / L.G, j = h * L.G + r % L.G;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(L.q) + u * L.qs.unit +
-                                 j * L.qs.head + node * L.qs.token;
-      for (int c = lane; c < kD; c += 32) q[c] = __bfloat162float(src[c]);
-      __syncwarp();
-      float* st = a.part + ((uh * a.rows + r) * a.nsplit + split) * kTreePart;
-      float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-      if (tile != t0) {
-        m = st[0];
-        l = st[1];
-        for (int c = 0; c < 4; ++c) o[c] = st[2 + lane + 32 * c];
-      }
-      float s[4], mt = -INFINITY;
-      for (int k = 0; k < 4; ++k) {
-        const int tk = lane + 32 * k;
-        float d = 0.f;
-        for (int c = 0; c < kD; ++c) d = __fmaf_rn(q[c], ks[tk * kTreePitch + c], d);
-        const bool ok = tile + tk < t1 && tree_vec(L, L.k_in, u, h, tile + tk) >= 0;
-        s[k] = ok ? d * (L.scale * kLog2e) : -INFINITY;
-        mt = fmaxf(mt, s[k]);
-      }
-      for (int x = 16; x >= 1; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-      const float mn = fmaxf(m, mt), ref = mn == -INFINITY ? 0.f : mn;
-      const float al = exp2f(m - ref);
-      float ls = 0.f;
-      for (int k = 0; k < 4; ++k) {
-        const float e = exp2f(s[k] - ref);
-        p[lane + 32 * k] = e;
-        ls += e;
-      }
-      for (int x = 16; x >= 1; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
-      __syncwarp();
-      for (int c = 0; c < 4; ++c) o[c] *= al;
-      for (int tk = 0; tk < kTreeTile; ++tk)
-        for (int c = 0; c < 4; ++c)
-          o[c] = __fmaf_rn(p[tk], vs[tk * kTreePitch + lane + 32 * c], o[c]);
-      __syncwarp();
-      if (lane == 0) {
-        st[0] = mn;
-        st[1] = __fmaf_rn(l, al, ls);
-      }
-      for (int c = 0; c < 4; ++c) st[2 + lane + 32 * c] = o[c];
-    }
+    out[x * 128] = make_uint4(e[0], e[1], e[2], e[3]);
   }
 }
 
-// One warp per row: merge the splits, then attend the draft nodes that the
-// row sees one by one (fp32), lane l holding coordinates l, l+32, l+64, l+96.
+// ------------------------------------------------------------------- codes
+// 32 consecutive codes as 16 f16 pairs.  A code sits in the mantissa of an f16
+// whose exponent is that of 1024, at bit d >= 1 (1024 + j 2^d), two codes 16
+// bits apart per register, so one AND-OR turns a shifted view of the words
+// into a pair and one exact fma into 2j - (2^b - 2):
+//   b = 3: pairs (a, a+5) of each run of ten codes (15 bits apart: d differs
+//          by one between the lanes), the last pair (30, 31) from its own bits;
+//   b = 2: pairs (i, i+8) of each word.
+// tree_slot gives the code that slot p of the 32 holds.
+template <int BITS>
+__host__ __device__ constexpr int tree_slot(int p) {
+  const int q = p >> 1, lane = p & 1;
+  if (BITS == 2) return 16 * (q >> 3) + (q & 7) + 8 * lane;
+  return q < 15 ? 10 * (q / 5) + q % 5 + 5 * lane : 30 + lane;
+}
+
+// f16 bits of +-2^e * m for values that f16 holds exactly (compile time).
+__host__ __device__ constexpr uint32_t f16_bits(float v) {
+  uint32_t s = 0;
+  if (v < 0) {
+    s = 0x8000u;
+    v = -v;
+  }
+  int e = 15;
+  while (v >= 2.0f) {
+    v *= 0.5f;
+    ++e;
+  }
+  while (v < 1.0f) {
+    v *= 2.0f;
+    --e;
+  }
+  return s | (static_cast<uint32_t>(e) << 10) | static_cast<uint32_t>((v - 1.0f) * 1024.0f);
+}
+__host__ __device__ constexpr uint32_t f16_pair(float lo, float hi) { return f16_bits(lo) | (f16_bits(hi) << 16); }
+
+__device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// The pair with fields at bits dl (low lane) and 16 + dh of v -> 2j - (2^b - 2).
+template <int BITS, int DL, int DH>
+__device__ __forceinline__ uint32_t tree_pair(uint32_t v) {
+  constexpr uint32_t kMask = (((1u << BITS) - 1u) << DL) | (((1u << BITS) - 1u) << (16 + DH));
+  constexpr float kOff = static_cast<float>((1 << BITS) - 2);
+  constexpr float kScaleL = 2.0f / (1 << DL), kScaleH = 2.0f / (1 << DH);
+  constexpr uint32_t kMul = f16_pair(kScaleL, kScaleH);
+  constexpr uint32_t kAdd = f16_pair(-(1024.0f * kScaleL + kOff), -(1024.0f * kScaleH + kOff));
+  return hfma2u((v & kMask) | 0x64006400u, kMul, kAdd);
+}
+
+template <int BITS>
+__device__ __forceinline__ void tree_unpack(const uint32_t (&w)[BITS], uint32_t (&h)[16]) {
+  if constexpr (BITS == 2) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const uint32_t v0 = w[m] << 1, v1 = w[m] >> 7;
+      h[8 * m] = tree_pair<2, 1, 1>(v0);
+      h[8 * m + 1] = tree_pair<2, 3, 3>(v0);
+      h[8 * m + 2] = tree_pair<2, 5, 5>(v0);
+      h[8 * m + 3] = tree_pair<2, 7, 7>(v0);
+      h[8 * m + 4] = tree_pair<2, 1, 1>(v1);
+      h[8 * m + 5] = tree_pair<2, 3, 3>(v1);
+      h[8 * m + 6] = tree_pair<2, 5, 5>(v1);
+      h[8 * m + 7] = tree_pair<2, 7, 7>(v1);
+    }
+  } else {
+    auto window = [&](int s) -> uint32_t {  // bits [s, s + 32) of the 96
+      if (s < 0) return w[0] << (-s);
+      const int i = s >> 5, o = s & 31;
+      const uint32_t lo = w[i], hi = i + 1 < 3 ? w[i + 1 < 3 ? i + 1 : 2] : 0u;
+      return o == 0 ? lo : __funnelshift_r(lo, hi, o);
+    };
+#pragma unroll
+    for (int b = 0; b < 3; ++b) {
+      const uint32_t v0 = window(30 * b - 2), v1 = window(30 * b + 4), v2 = window(30 * b + 10);
+      h[5 * b] = tree_pair<3, 2, 1>(v0);
+      h[5 * b + 1] = tree_pair<3, 5, 4>(v0);
+      h[5 * b + 2] = tree_pair<3, 2, 1>(v1);
+      h[5 * b + 3] = tree_pair<3, 5, 4>(v1);
+      h[5 * b + 4] = tree_pair<3, 2, 1>(v2);
+    }
+    h[15] = tree_pair<3, 2, 1>(((w[2] >> 24) & 0x1Cu) | ((w[2] >> 12) & 0xE0000u));
+  }
+}
+
+// This thread's BITS words (32 codes) of a staged row.
+template <int BITS>
+__device__ __forceinline__ void tree_words(uint32_t addr, uint32_t (&w)[BITS]) {
+#pragma unroll
+  for (int i = 0; i < BITS; ++i) w[i] = lds32(addr + 4 * i);
+}
+
+// Row t, 16-byte chunk c of an operand of 128-byte swizzled rows (the K-major
+// layout with a token per row and the MN-major one with a token per k are the
+// same addresses).
+__device__ __forceinline__ uint32_t row_chunk(int t, int c) {
+  return static_cast<uint32_t>((t >> 3) * 1024 + (t & 7) * 128 + ((c ^ (t & 7)) << 4));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ------------------------------------------------------------ shared memory
+template <int BK, int BV, int NR>
+struct TreeSmem {
+  static constexpr int N = 4 * NR;
+  static constexpr int T = 0;                           // t of the keys: 2 x (128 rows x 128 B)
+  static constexpr int K = T + 32768;                   // rotated keys, the same
+  static constexpr int V = K + 32768;                   // scaled value codes
+  static constexpr int P = V + 32768;                   // weights: N/64 blocks of 128 rows
+  static constexpr int Q = P + (N > 64 ? 2 : 1) * 16384;  // queries: 2 x (N rows x 128 B)
+  static constexpr int H = Q + N * 256;                 // H64, 64 rows x 128 B
+  static constexpr int CA = H + 8192;                   // coset bits of the tile, 128 x 16 f16
+  static constexpr int CB = CA + 4096;                  // their rows of H, 128 x 16 f16
+  static constexpr int Stage = CB + 4096;
+  static constexpr int KC = 128 * 16 * BK, VC = 128 * 16 * BV;
+  static constexpr int StageBytes = KC + VC + 3 * 512;  // codes, key meta, value meta, validity
+  static constexpr int FM = Stage + kTreeStages * StageBytes;  // (f0, f1, -m0, -m1) per row pair
+  static constexpr int WMax = FM + N * 8;               // [4 warpgroups][NR][4 warps]
+  static constexpr int Vec = WMax + N * 16;             // staging warp: vector indexes of a tile
+  static constexpr int Bars = Vec + 2048;
+  static constexpr int Bytes = Bars + 128 + 1024;       // 1 KB of slack to align the base
+  static_assert(Bytes <= 232448, "one CTA per SM within 227 KB");
+};
+
+// Bounded wait; past the limit the error word is set and `dead` makes every
+// later wait of the CTA return at once (its results are then unspecified).
+__device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
+  bool done = mbar_try_wait(bar, parity);
+  for (uint32_t spin = 0; !done && spin < kTreeWaitLimit; ++spin)
+    done = mbar_try_wait(bar, parity) || *dead;
+  if (!done) {
+    *dead = 1u;
+    atomicOr(&g_nq_error, kErrTreeTimeout);
+  }
+  __syncwarp();
+}
+
+template <int BK, int BV, int NR>
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const TreeArgs a) {
+  using S = TreeSmem<BK, BV, NR>;
+  constexpr int N = S::N;
+  extern __shared__ __align__(1024) unsigned char tree_smem[];
+  const uint32_t raw = smem_u32(tree_smem);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* gen = tree_smem + (base - raw);  // generic pointer of the aligned base
+  const TreeLaunch& L = a.L;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bar_x = base + S::Bars, bar_s = bar_x + 8, bar_o = bar_x + 16;
+  const uint32_t full = bar_x + 24, empty = full + 8 * kTreeStages;
+  const uint32_t tslot = empty + 8 * kTreeStages;
+  volatile uint32_t* dead = reinterpret_cast<volatile uint32_t*>(gen + (tslot + 4 - base));
+
+  // block index -> (split, unit * heads + head, row block): the row blocks and
+  // heads of the same tokens are neighbours (their codes and angles meet in L2)
+  const int rb = static_cast<int>(blockIdx.x % a.rblocks);
+  const int64_t rest = blockIdx.x / a.rblocks;
+  const int64_t UH = static_cast<int64_t>(L.units) * L.heads;
+  const int64_t uh = rest % UH, split = rest / UH;
+  const int64_t u = uh / L.heads;
+  const int h = static_cast<int>(uh % L.heads);
+  const int64_t len = tree_len(L, u);
+  const int64_t t0 = split * a.per * kTreeTile, t1 = min64(t0 + a.per * kTreeTile, len);
+  const int nt = t1 > t0 ? static_cast<int>((t1 - t0 + kTreeTile - 1) / kTreeTile) : 0;
+  const int row0 = rb * N;
+  float* part = a.part + ((uh * a.rows + row0) * a.nsplit + split) * kTreePart;
+  const int64_t part_row = a.nsplit * kTreePart;
+
+  if (nt == 0) {  // nothing held in this split
+    if (tid < N && row0 + tid < a.rows) {
+      part[tid * part_row] = -INFINITY;
+      part[tid * part_row + 1] = 0.f;
+    }
+    return;
+  }
+
+  // ---- setup: barriers, TMEM, constant operands, queries
+  constexpr uint32_t kCols = 128 + 2 * N <= 256 ? 256u : 512u;  // X, S, O
+  if (warp == 16) {
+    tmem_alloc(tslot, kCols);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    mbar_init(bar_x, 1);
+    mbar_init(bar_s, 1);
+    mbar_init(bar_o, 1);
+    for (int s = 0; s < kTreeStages; ++s) {
+      mbar_init(full + 8 * s, 64);   // each staging lane: its copies, its stores
+      mbar_init(empty + 8 * s, 16);  // each compute warp
+    }
+    *dead = 0u;
+    fence_mbar_init();
+  }
+  if (tid < 512) {  // H64: row n, chunk c (8 slots)
+    const int n = tid >> 3, c = tid & 7;
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t pr = 0u;
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        const int s = 8 * c + 2 * i + l;
+        const int code = 32 * (s >> 5) + tree_slot<BK>(s & 31);
+        pr |= (0x3C00u | (static_cast<uint32_t>(__popc(n & code) & 1) << 15)) << (16 * l);
+      }
+      v[i] = pr;
+    }
+    sts128(base + S::H + row_chunk(n, c), make_uint4(v[0], v[1], v[2], v[3]));
+  }
+  if (tid < 256) {  // coset slots: output row n, groups 8c .. 8c+7 (u rows: c = 0, v rows: c = 1)
+    const int n = tid >> 1, c = tid & 1;
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    if ((n >> 6) == c && (n & 7) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t s0 = __popc(n & 63 & (8 * (2 * i))) & 1, s1 = __popc(n & 63 & (8 * (2 * i + 1))) & 1;
+        v[i] = (s0 ? 0x4800u : 0xC800u) | ((s1 ? 0x4800u : 0xC800u) << 16);  // -8 (-1)^popc
+      }
+    }
+    sts128(base + S::CB + c * 2048 + n * 16, make_uint4(v[0], v[1], v[2], v[3]));
+  }
+  if (warp < 16) {
+    for (int r = warp; r < N; r += 16) {
+      const int row = row0 + r;
+      float q[4] = {0.f, 0.f, 0.f, 0.f};
+      if (row < a.rows) {
+        const int node = row / L.G, j = h * L.G + row % L.G;
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(
+                                  static_cast<const uint16_t*>(L.q) + u * L.qs.unit +
+                                  j * L.qs.head + node * L.qs.token) + lane);
+        q[0] = bf16lo(v.x);
+        q[1] = bf16hi(v.x);
+        q[2] = bf16lo(v.y);
+        q[3] = bf16hi(v.y);
+      }
+      float m = fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])));
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // |q| 2^-e in [2^13, 2^14): bf16 values fit f16 exactly down to 2^-24 of
+      // that scale's 2^-14, i.e. 2^-28 of the row's largest before any rounding
+      const int e = m > 0.f && m < INFINITY ? static_cast<int>(__float_as_uint(m) >> 23) - 127 - 13 : 0;
+      const float down = e >= -126 && e <= 126 ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.f;
+      const __half2 p0 = __floats2half2_rn(q[0] * down, q[1] * down);
+      const __half2 p1 = __floats2half2_rn(q[2] * down, q[3] * down);
+      const int c = lane >> 1;  // chunk of 8 coordinates, this lane's half of it
+      const uint32_t dst = base + S::Q + (c >> 3) * (N * 128) + row_chunk(r, c & 7) + (lane & 1) * 8;
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst),
+                   "r"(*reinterpret_cast<const uint32_t*>(&p0)),
+                   "r"(*reinterpret_cast<const uint32_t*>(&p1))
+                   : "memory");
+      if (lane == 0) {
+        float* fm = reinterpret_cast<float*>(gen + S::FM) + (r >> 1) * 4 + (r & 1);
+        const float up = down > 0.f ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 0.f;
+        fm[0] = L.scale * kLog2e * up;
+        fm[2] = 0.f;
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = lds32(tslot);
+  const uint32_t tX = tmem, tS = tmem + 128, tO = tmem + 128 + N;
+
+  if (warp == 17) {
+    // ------------------------------------------------------------- staging
+    int64_t* vec = reinterpret_cast<int64_t*>(gen + S::Vec);
+    for (int j = 0; j < nt; ++j) {
+      const int s = j % kTreeStages;
+      if (j >= kTreeStages) tree_wait(empty + 8 * s, ((j / kTreeStages) - 1) & 1, dead);
+      const uint32_t st = base + S::Stage + s * S::StageBytes;
+      float* inv = reinterpret_cast<float*>(gen + S::Stage + s * S::StageBytes + S::KC + S::VC + 1024);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tk = lane + 32 * i;
+        const int64_t t = t0 + static_cast<int64_t>(j) * kTreeTile + tk;
+        int64_t vk = -1, vv = -1;
+        if (t < t1) {
+          if (!L.table) {
+            vk = u * L.k_in.unit_stride + h * L.k_in.head_stride + t;
+            vv = u * L.v_in.unit_stride + h * L.v_in.head_stride + t;
+          } else {
+            const uint32_t pj = static_cast<uint32_t>(t) / static_cast<uint32_t>(L.page_size);
+            const int64_t page = __ldg(L.table + u * L.table_stride + pj);
+            if (page >= 0 && page < L.pages) {
+              const int64_t off = t - static_cast<int64_t>(pj) * L.page_size;
+              vk = page * L.k_in.unit_stride + h * L.k_in.head_stride + off;
+              vv = page * L.v_in.unit_stride + h * L.v_in.head_stride + off;
+            }
+          }
+        }
+        vec[tk] = vk;
+        vec[128 + tk] = vv;
+        inv[tk] = vk >= 0 ? 0.f : -INFINITY;
+        const uint32_t mb = vk >= 0 ? 4u : 0u;  // bytes to copy, the rest is zero-filled
+        const uint32_t md = st + S::KC + S::VC + tk * 4;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(md),
+                     "l"(L.k_in.meta + (vk < 0 ? 0 : vk)), "r"(mb)
+                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(md + 512),
+                     "l"(L.v_in.meta + (vv < 0 ? 0 : vv)), "r"(mb)
+                     : "memory");
+      }
+      __syncwarp();
+      auto copy = [&](const uint32_t* codes, int bits, const int64_t* vx, uint32_t dst) {
+        for (int c = lane; c < 128 * bits; c += 32) {
+          const int tk = c / bits;
+          const int64_t v = vx[tk];
+          const uint32_t* src = codes + (v < 0 ? 0 : v) * (4 * bits) + (c - tk * bits) * 4;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + c * 16), "l"(src),
+                       "r"(v < 0 ? 0u : 16u)
+                       : "memory");
+        }
+      };
+      copy(L.k_in.codes, BK, vec, st);
+      copy(L.v_in.codes, BV, vec + 128, st + S::KC);
+      mbar_arrive_cp_async(full + 8 * s);
+      mbar_arrive(full + 8 * s);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else if (warp == 16) {
+    // ------------------------------------------------------------ the MMAs
+    constexpr uint32_t iX = idesc_f16_f32(128, 64), iC = idesc_f16_f32(128, 128);
+    constexpr uint32_t iS = idesc_f16_f32(128, N), iO = idesc_f16_f32(128, N) | kIdescAMn | kIdescBMn;
+    auto mma_x = [&]() {
+      umma_f16(tX, desc_plain(base + S::CA, 2048, 128), desc_plain(base + S::CB, 2048, 128), iC, 0u);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_f16(tX + 64 * hf, desc_sw128(base + S::T + hf * 16384 + k * 32),
+                   desc_sw128(base + S::H + k * 32), iX, 1u);
+      umma_commit(bar_x);
+    };
+    auto mma_s = [&]() {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_f16(tS, desc_sw128(base + S::K + (k >> 2) * 16384 + (k & 3) * 32),
+                 desc_sw128(base + S::Q + (k >> 2) * (N * 128) + (k & 3) * 32), iS, k > 0);
+      umma_commit(bar_s);
+    };
+    auto mma_o = [&](bool acc) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_f16(tO, desc_sw128_mn(base + S::V + k * 2048, 16384),
+                 desc_sw128_mn(base + S::P + k * 2048, 16384), iO, acc || k > 0);
+      umma_commit(bar_o);
+    };
+    constexpr uint32_t kAll = 512 + 32;
+    named_bar_sync(5, kAll);
+    tc_fence_after();
+    if (lane == 0) mma_x();
+    named_bar_sync(7, kAll);
+    tc_fence_after();
+    if (lane == 0) mma_s();
+    for (int j = 0; j < nt; ++j) {
+      if (j + 1 < nt) {
+        named_bar_sync(5, kAll);
+        tc_fence_after();
+        if (lane == 0) mma_x();
+      }
+      named_bar_sync(6, kAll);
+      tc_fence_after();
+      if (lane == 0) mma_o(j > 0);
+      if (j + 1 < nt) {
+        named_bar_sync(7, kAll);
+        tc_fence_after();
+        if (lane == 0) mma_s();
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------ compute threads
+    constexpr uint32_t kAll = 512 + 32;
+    const int w = tid >> 7, t = tid & 127, wl = warp & 3;
+    const uint32_t t_lane = static_cast<uint32_t>(32 * wl) << 16;
+    const uint4* ang = a.angles + u * a.angle_stride +
+                       ((split * a.per * 4 + w) * 4) * 128 + t;  // tile 0 of the split
+    auto stage_of = [&](int j) { return base + S::Stage + (j % kTreeStages) * S::StageBytes; };
+
+    // keys of tile j -> T and coset slots
+    auto write_t = [&](int j, float& kap, bool& valid) {
+      const uint32_t st = stage_of(j);
+      tree_wait(full + 8 * (j % kTreeStages), (j / kTreeStages) & 1, dead);
+      uint32_t wd[BK], hh[16];
+      tree_words<BK>(st + t * (16 * BK) + w * (4 * BK), wd);
+      const uint32_t meta = lds32(st + S::KC + S::VC + t * 4);
+      valid = lds32(st + S::KC + S::VC + 1024 + t * 4) == 0u;
+      tree_unpack<BK>(wd, hh);
+      const uint32_t dst = base + S::T + (w >> 1) * 16384;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        sts128(dst + row_chunk(t, (w & 1) * 4 + c),
+               make_uint4(hh[4 * c], hh[4 * c + 1], hh[4 * c + 2], hh[4 * c + 3]));
+      // coset bits 4w .. 4w+3 as f16 0 or 1
+      const uint32_t cm = meta >> (4 * w);
+      const uint32_t c01 = ((cm & 1u) * 0x3C00u) | (((cm >> 1) & 1u) * 0x3C000000u);
+      const uint32_t c23 = (((cm >> 2) & 1u) * 0x3C00u) | (((cm >> 3) & 1u) * 0x3C000000u);
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(base + S::CA + (w >> 1) * 2048 + t * 16 +
+                                                              (w & 1) * 8),
+                   "r"(c01), "r"(c23)
+                   : "memory");
+      const float sig = __half2float(__ushort_as_half(static_cast<unsigned short>(meta >> 16)));
+      kap = __fmul_rn(__fmul_rn(sig, 0.5f), __uint_as_float(kCBits));
+      fence_proxy_async_smem();
+      tc_fence_before();
+      named_bar_arrive(5, kAll);
+    };
+    // X of tile j -> rotated keys
+    auto write_k = [&](const uint4 (&cs)[4], uint32_t par) {
+      tree_wait(bar_x, par, dead);
+      tc_fence_after();
+      uint32_t uu[16], vv[16];
+      tmem_ld(tX + t_lane + 16 * w, uu);
+      tmem_ld(tX + t_lane + 64 + 16 * w, vv);
+      tmem_wait_ld(uu);
+      tmem_wait_ld(vv);
+      uint32_t lo[8], hi[8];
+#pragma unroll
+      for (int f = 0; f < 8; ++f) {
+        const uint32_t cw = (f & 1) ? cs[f >> 1].z : cs[f >> 1].x;
+        const uint32_t sw = (f & 1) ? cs[f >> 1].w : cs[f >> 1].y;
+        const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&cw));
+        const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw));
+        const float2 U = make_float2(__uint_as_float(uu[2 * f]), __uint_as_float(uu[2 * f + 1]));
+        const float2 V = make_float2(__uint_as_float(vv[2 * f]), __uint_as_float(vv[2 * f + 1]));
+        const float2 a0 = fma2(U, c, mul2(V, s));
+        const float2 vc = mul2(V, c);
+        const float2 a1 = fma2(U, s, make_float2(-vc.x, -vc.y));
+        const __half2 p0 = __floats2half2_rn(a0.x, a0.y), p1 = __floats2half2_rn(a1.x, a1.y);
+        lo[f] = *reinterpret_cast<const uint32_t*>(&p0);
+        hi[f] = *reinterpret_cast<const uint32_t*>(&p1);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t dst = base + S::K + row_chunk(t, 2 * w + c);
+        sts128(dst, make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]));
+        sts128(dst + 16384, make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]));
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      named_bar_arrive(7, kAll);
+    };
+    // values of tile j -> V, and the stage is free
+    auto write_v = [&](int j, float& vm) {
+      const uint32_t st = stage_of(j);
+      uint32_t wd[BV], hh[16];
+      tree_words<BV>(st + S::KC + t * (16 * BV) + w * (4 * BV), wd);
+      const uint32_t meta = lds32(st + S::KC + S::VC + 512 + t * 4);
+      tree_unpack<BV>(wd, hh);
+      // sigma = 2^e m with e >= -22 (so that 2^(e-2) t is exact in f16), 1 <= m < 2
+      // (or below for the smallest scales); 7 * 2^13 stays in range
+      const float sig = __half2float(__ushort_as_half(static_cast<unsigned short>(meta >> 16)));
+      const int e = max(static_cast<int>(__float_as_uint(sig) >> 23) - 127, -22);
+      vm = sig * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const uint32_t s16 = __half_as_ushort(
+          __float2half_rn(__uint_as_float(static_cast<uint32_t>(125 + e) << 23)));
+      const uint32_t ss = s16 | (s16 << 16);
+      // byte g of z has coset bit g of this quarter in its top bit; a byte
+      // permute that repeats top bits makes the -2^(e-2) lanes of the set groups
+      const uint32_t z = ((meta >> (4 * w)) & 15u) * 0x10204080u;
+      const uint32_t neg = ss ^ 0x80008000u;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int ga = tree_slot<BV>(2 * q) >> 3, gb = tree_slot<BV>(2 * q + 1) >> 3;
+        uint32_t m;  // (prmt's sign mode: __byte_perm has no form of it)
+        asm("prmt.b32 %0, %1, %1, %2;" : "=r"(m) : "r"(z), "r"(0x8888u | (ga * 0x11u) | (gb * 0x1100u)));
+        hh[q] = hfma2u(hh[q], ss, neg & m);
+      }
+      const uint32_t dst = base + S::V + (w >> 1) * 16384;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        sts128(dst + row_chunk(t, (w & 1) * 4 + c),
+               make_uint4(hh[4 * c], hh[4 * c + 1], hh[4 * c + 2], hh[4 * c + 3]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * (j % kTreeStages));
+    };
+
+    float l[NR];
+#pragma unroll
+    for (int c = 0; c < NR; ++c) l[c] = 0.f;
+    bool started = false;  // some token of the split was valid (per warpgroup)
+    float4* fm = reinterpret_cast<float4*>(gen + S::FM) + w * (NR / 2);
+    int* wmax = reinterpret_cast<int*>(gen + S::WMax) + w * (NR * 4);
+
+    float kap, kap_next = 0.f, vm;
+    bool valid, valid_next = false;
+    uint4 cs[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) cs[x] = __ldg(ang + x * 128);
+    write_t(0, kap, valid);
+    write_k(cs, 0u);
+    write_v(0, vm);
+
+    for (int j = 0; j < nt; ++j) {
+      if (j + 1 < nt) {
+        write_t(j + 1, kap_next, valid_next);
+        ang += 16 * 128;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) cs[x] = __ldg(ang + x * 128);
+      }
+      // ---- softmax of tile j
+      tree_wait(bar_s, j & 1, dead);
+      tc_fence_after();
+      float y[NR];
+      constexpr int CH = NR < 16 ? NR : 16;
+#pragma unroll
+      for (int c0 = 0; c0 < NR; c0 += CH) {
+        uint32_t s[CH];
+        tmem_ld(tS + t_lane + w * NR + c0, s);
+        tmem_wait_ld(s);
+#pragma unroll
+        for (int c = 0; c < CH; c += 2) {
+          const float4 f = fm[(c0 + c) / 2];
+          const float2 g = mul2(make_float2(f.x, f.y), make_float2(kap, kap));
+          const float2 v = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), g,
+                                make_float2(f.z, f.w));
+          y[c0 + c] = v.x;
+          y[c0 + c + 1] = v.y;
+        }
+      }
+      if (!valid) {
+#pragma unroll
+        for (int c = 0; c < NR; ++c) y[c] = -INFINITY;
+      }
+      float top = y[0];
+#pragma unroll
+      for (int c = 1; c < NR; ++c) top = fmaxf(top, y[c]);
+      if (named_bar_or(1 + w, 128, top > 14.0f || (!started && valid))) {
+        // exact column maxima of the tile, as ordered integers
+#pragma unroll
+        for (int c = 0; c < NR; ++c) {
+          const int i = __float_as_int(y[c]);
+          const int k = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
+          if (lane == 0) wmax[c * 4 + wl] = k;
+        }
+        named_bar_sync(1 + w, 128);
+        auto delta_of = [&](int c) {
+          const int4 k4 = *reinterpret_cast<const int4*>(wmax + c * 4);
+          const int k = max(max(k4.x, k4.y), max(k4.z, k4.w));
+          const float d = __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)) - 6.0f;
+          return started ? fmaxf(d, 0.f) : d;
+        };
+        if (t < NR) {
+          float* m = reinterpret_cast<float*>(fm + (t >> 1)) + 2 + (t & 1);
+          *m -= delta_of(t);
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < NR; c0 += 4) {
+          float al[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float d = delta_of(c0 + c);
+            y[c0 + c] -= d;
+            al[c] = ex2(-d);
+            l[c0 + c] = started ? l[c0 + c] * al[c] : 0.f;
+          }
+          if (started && j > 0) {
+            uint32_t o[4];
+            tmem_ld(tO + t_lane + w * NR + c0, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
+            tmem_st(tO + t_lane + w * NR + c0, o);
+          }
+        }
+        tmem_wait_st();
+        started = true;
+        named_bar_sync(1 + w, 128);  // the references are written, wmax is free
+      }
+      {
+        constexpr int kPB = NR >= 8 ? 8 : 4;  // rows per store
+        const uint32_t dst = base + S::P + (w * NR / 64) * 16384;
+#pragma unroll
+        for (int c0 = 0; c0 < NR; c0 += kPB) {
+          uint32_t pk[kPB / 2];
+#pragma unroll
+          for (int c = 0; c < kPB; c += 2) {
+            const float2 p = make_float2(ex2(y[c0 + c]), ex2(y[c0 + c + 1]));
+            const float2 s2 = add2(make_float2(l[c0 + c], l[c0 + c + 1]), p);
+            l[c0 + c] = s2.x;
+            l[c0 + c + 1] = s2.y;
+            const float2 pm = mul2(p, make_float2(vm, vm));
+            const __half2 ph = __floats2half2_rn(pm.x, pm.y);
+            pk[c / 2] = *reinterpret_cast<const uint32_t*>(&ph);
+          }
+          const int col = (w * NR + c0) % 64;
+          const uint32_t ad = dst + row_chunk(t, col >> 3) + (col & 7) * 2;
+          if constexpr (kPB == 8)
+            sts128(ad, make_uint4(pk[0], pk[1], pk[2], pk[3]));
+          else
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(ad), "r"(pk[0]), "r"(pk[1])
+                         : "memory");
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      named_bar_arrive(6, kAll);
+      if (j + 1 < nt) {
+        write_k(cs, (j + 1) & 1);
+        tree_wait(bar_o, j & 1, dead);  // V and P of tile j have been read
+        tc_fence_after();
+        write_v(j + 1, vm);
+      }
+      kap = kap_next;
+      valid = valid_next;
+    }
+    tree_wait(bar_o, (nt - 1) & 1, dead);
+    tc_fence_after();
+
+    // ---- the split's sums: lane = code coordinate of this thread's TMEM lane
+    const int coord = 32 * (t >> 5) + tree_slot<BV>(t & 31);
+#pragma unroll
+    for (int c0 = 0; c0 < NR; c0 += 4) {
+      uint32_t o[4];
+      tmem_ld(tO + t_lane + w * NR + c0, o);
+      tmem_wait_ld(o);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int r = w * NR + c0 + c;
+        if (row0 + r < a.rows) part[r * part_row + 2 + coord] = __uint_as_float(o[c]);
+      }
+    }
+    float* wsum = reinterpret_cast<float*>(wmax);
+#pragma unroll
+    for (int c = 0; c < NR; ++c) {
+      float s = l[c];
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) wsum[c * 4 + wl] = s;
+    }
+    named_bar_sync(1 + w, 128);
+    if (t < NR && row0 + w * NR + t < a.rows) {
+      const float4 s = *reinterpret_cast<const float4*>(wsum + t * 4);
+      const float* m = reinterpret_cast<const float*>(fm + (t >> 1)) + 2 + (t & 1);
+      float* p = part + (w * NR + t) * part_row;
+      p[0] = started ? -*m : -INFINITY;
+      p[1] = (s.x + s.y) + (s.z + s.w);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+// One warp per row: merge the splits, transform, then attend the draft nodes
+// that the row sees one by one (fp32).  Lane l holds coordinates l, l+32,
+// l+64, l+96: Hadamard stages 1..16 across lanes, 32 and 64 in the lane.
 __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a) {
   const TreeLaunch& L = a.L;
   const int lane = threadIdx.x & 31;
@@ -160,14 +784,35 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a) {
   const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(L.q) + u * L.qs.unit +
                             j * L.qs.head + node * L.qs.token;
   float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+#pragma unroll
   for (int c = 0; c < 4; ++c) q[c] = __bfloat162float(qp[lane + 32 * c]) * (L.scale * kLog2e);
-  for (int64_t s = 0; s < a.nsplit; ++s) {
-    const float* p = a.part + (w * a.nsplit + s) * kTreePart;
-    const float mn = fmaxf(m, p[0]), ref = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(m - ref), g = exp2f(p[0] - ref);
-    l = l * f + g * p[1];
-    for (int c = 0; c < 4; ++c) o[c] = o[c] * f + g * p[2 + lane + 32 * c];
-    m = mn;
+  const float* p0 = a.part + w * a.nsplit * kTreePart;
+  for (int64_t s = 0; s < a.nsplit; ++s) m = fmaxf(m, p0[s * kTreePart]);
+  if (m > -INFINITY) {
+    for (int64_t s = 0; s < a.nsplit; ++s) {
+      const float* p = p0 + s * kTreePart;
+      if (p[0] == -INFINITY) continue;  // no token in it: its sums were not written
+      const float f = exp2f(p[0] - m);
+      l = __fmaf_rn(f, p[1], l);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c] = __fmaf_rn(f, p[2 + lane + 32 * c], o[c]);
+    }
+#pragma unroll
+    for (int st = 1; st < 32; st <<= 1) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float x = __shfl_xor_sync(0xffffffffu, o[c], st);
+        o[c] = (lane & st) ? x - o[c] : o[c] + x;
+      }
+    }
+    // the sums are of sigma t / 4: v = (sigma / 2) C H t
+    const float k = 2.0f * __uint_as_float(kCBits);
+    const float x0 = (o[0] + o[1]) * k, x1 = (o[0] - o[1]) * k;
+    const float x2 = (o[2] + o[3]) * k, x3 = (o[2] - o[3]) * k;
+    o[0] = x0 + x2;
+    o[2] = x0 - x2;
+    o[1] = x1 + x3;
+    o[3] = x1 - x3;
   }
   const int words = (L.nodes + 63) / 64;
   for (int x = 0; x < words; ++x) {
@@ -182,56 +827,98 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a) {
       const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(L.V_new) + u * L.vns.unit +
                                 h * L.vns.head + k * L.vns.token;
       float s = 0.f;
+#pragma unroll
       for (int c = 0; c < 4; ++c) s = __fmaf_rn(q[c], __bfloat162float(kp[lane + 32 * c]), s);
+#pragma unroll
       for (int x2 = 16; x2 >= 1; x2 >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x2);
       const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
       const float f = exp2f(m - ref), g = exp2f(s - ref);
-      l = l * f + g;
-      for (int c = 0; c < 4; ++c) o[c] = o[c] * f + g * __bfloat162float(vp[lane + 32 * c]);
+      l = __fmaf_rn(l, f, g);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        o[c] = __fmaf_rn(o[c], f, g * __bfloat162float(vp[lane + 32 * c]));
       m = mn;
     }
   }
   const float inv = l > 0.f ? 1.0f / l : 0.f;
   __nv_bfloat16* op = static_cast<__nv_bfloat16*>(L.out) + u * L.os.unit + j * L.os.head +
                       node * L.os.token;
+#pragma unroll
   for (int c = 0; c < 4; ++c) op[lane + 32 * c] = __float2bfloat16_rn(o[c] * inv);
   if (L.lse && lane == 0)
     L.lse[(u * L.heads * L.G + j) * L.nodes + node] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-static int64_t tree_chunk(int units, int heads, int64_t n) {
-  const int64_t uh = static_cast<int64_t>(units) * heads;
-  const int64_t want = uh > 0 ? (2 * 148 + uh - 1) / uh : 1;
-  int64_t chunk = (n + want - 1) / want;
-  chunk = (chunk + kTreeTile - 1) / kTreeTile * kTreeTile;
-  return chunk < kTreeTile ? kTreeTile : chunk;
+// ------------------------------------------------------------------ launch
+struct TreePlan {
+  int nr, rblocks;
+  int64_t tiles, per, nsplit;
+};
+
+// Rows per CTA: up to 128 columns, blocks of equal width for more rows.
+// Splits: the launch costs (waves of 148 CTAs) * (tiles per CTA + setup, about
+// two tiles); the smallest cost, the fewest splits among equals.
+static TreePlan tree_plan(int units, int heads, int G, int nodes, int64_t n) {
+  TreePlan p{};
+  const int64_t rows = static_cast<int64_t>(nodes) * G;
+  p.rblocks = static_cast<int>((rows + 127) / 128);
+  const int64_t cols = (rows + p.rblocks - 1) / p.rblocks;
+  p.nr = cols <= 16 ? 4 : (cols <= 32 ? 8 : (cols <= 64 ? 16 : 32));
+  p.rblocks = static_cast<int>((rows + 4 * p.nr - 1) / (4 * p.nr));
+  p.tiles = (n + kTreeTile - 1) / kTreeTile;
+  if (p.tiles < 1) p.tiles = 1;
+  const int64_t ctas = static_cast<int64_t>(units) * heads * p.rblocks;
+  int64_t best = -1;
+  for (int64_t s = 1; s <= p.tiles && s <= 4 * 148; ++s) {
+    const int64_t per = (p.tiles + s - 1) / s, ns = (p.tiles + per - 1) / per;
+    const int64_t cost = (ctas * ns + 147) / 148 * (per + 2);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.per = per;
+      p.nsplit = ns;
+    }
+    if (ctas * s >= 4 * 148 && s > 1) break;  // finer splits only add setup
+  }
+  return p;
 }
 
-static int64_t tree_splits(int units, int heads, int64_t n) {
-  const int64_t c = tree_chunk(units, heads, n);
-  return (n + c - 1) / c;
+static size_t tree_part_bytes(int units, int heads, int G, int nodes, const TreePlan& p) {
+  const size_t b = static_cast<size_t>(units) * heads * G * nodes * p.nsplit * kTreePart * sizeof(float);
+  return (b + 255) / 256 * 256;
 }
 
-size_t tree_workspace_bytes(int units, int heads, int G, int nodes, int64_t n, bool) {
-  return static_cast<size_t>(units) * heads * G * nodes * tree_splits(units, heads, n) *
-         kTreePart * sizeof(float);
+size_t tree_workspace_bytes(int units, int heads, int G, int nodes, int64_t n, bool shared) {
+  const TreePlan p = tree_plan(units, heads, G, nodes, n);
+  return tree_part_bytes(units, heads, G, nodes, p) +
+         static_cast<size_t>(shared ? 1 : units) * p.tiles * 16 * 128 * sizeof(uint4);
 }
 
 int64_t tree_ctas(int units, int heads, int G, int nodes, int64_t n) {
-  const int64_t uh = static_cast<int64_t>(units) * heads;
-  const int64_t a = uh * tree_splits(units, heads, n), b = (uh * G * nodes + 7) / 8;
+  const TreePlan p = tree_plan(units, heads, G, nodes, n);
+  const int64_t a = static_cast<int64_t>(units) * heads * p.rblocks * p.nsplit;
+  const int64_t b = static_cast<int64_t>(units) * p.tiles;
   return a > b ? a : b;
 }
 
-template <int BK, int BV>
-static cudaError_t launch_tree_partial(const TreeArgs& a, cudaStream_t stream) {
-  constexpr int smem = (2 * kTreeTile * kTreePitch + 16 * kD) * static_cast<int>(sizeof(float));
-  cudaError_t err = cudaFuncSetAttribute(tree_partial_kernel<BK, BV>,
+template <int BK, int BV, int NR>
+static cudaError_t launch_tree_nr(const TreeArgs& a, int64_t grid, cudaStream_t stream) {
+  constexpr int smem = TreeSmem<BK, BV, NR>::Bytes;
+  cudaError_t err = cudaFuncSetAttribute(tree_partial_kernel<BK, BV, NR>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  const int64_t grid = static_cast<int64_t>(a.L.units) * a.L.heads * a.nsplit;
-  tree_partial_kernel<BK, BV><<<static_cast<unsigned>(grid), 256, smem, stream>>>(a);
+  tree_partial_kernel<BK, BV, NR>
+      <<<static_cast<unsigned>(grid), kTreeThreads, smem, stream>>>(a);
   return cudaGetLastError();
+}
+
+template <int BK, int BV>
+static cudaError_t launch_tree_partial(const TreeArgs& a, int nr, int64_t grid, cudaStream_t stream) {
+  switch (nr) {
+    case 4: return launch_tree_nr<BK, BV, 4>(a, grid, stream);
+    case 8: return launch_tree_nr<BK, BV, 8>(a, grid, stream);
+    case 16: return launch_tree_nr<BK, BV, 16>(a, grid, stream);
+    default: return launch_tree_nr<BK, BV, 32>(a, grid, stream);
+  }
 }
 
 cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream) {
@@ -239,20 +926,41 @@ cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream) {
   a.L = L;
   a.rows = L.nodes * L.G;
   a.n_a = (L.rope_max_pos + 255) / 256;
-  a.chunk = tree_chunk(L.units, L.heads, L.n);
-  a.nsplit = tree_splits(L.units, L.heads, L.n);
-  a.part = static_cast<float*>(L.ws);
   if (L.n > 0) {
+    const TreePlan p = tree_plan(L.units, L.heads, L.G, L.nodes, L.n);
+    a.ncols = 4 * p.nr;
+    a.rblocks = p.rblocks;
+    a.tiles = p.tiles;
+    a.per = p.per;
+    a.nsplit = p.nsplit;
+    a.part = static_cast<float*>(L.ws);
+    a.angles = reinterpret_cast<uint4*>(static_cast<char*>(L.ws) +
+                                        tree_part_bytes(L.units, L.heads, L.G, L.nodes, p));
+    a.angle_stride = L.positions ? p.tiles * 16 * 128 : 0;
+    const int64_t agrid = p.tiles * (L.positions ? L.units : 1);
+    tree_angles_kernel<<<static_cast<unsigned>(agrid), 512, 0, stream>>>(a);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    const int64_t grid = static_cast<int64_t>(L.units) * L.heads * p.rblocks * p.nsplit;
     const int bk = L.k_in.bits, bv = L.v_in.bits;
-    const cudaError_t err = bk == 3 ? (bv == 3 ? launch_tree_partial<3, 3>(a, stream)
-                                               : launch_tree_partial<3, 2>(a, stream))
-                                    : (bv == 3 ? launch_tree_partial<2, 3>(a, stream)
-                                               : launch_tree_partial<2, 2>(a, stream));
+    err = bk == 3 ? (bv == 3 ? launch_tree_partial<3, 3>(a, p.nr, grid, stream)
+                             : launch_tree_partial<3, 2>(a, p.nr, grid, stream))
+                  : (bv == 3 ? launch_tree_partial<2, 3>(a, p.nr, grid, stream)
+                             : launch_tree_partial<2, 2>(a, p.nr, grid, stream));
     if (err != cudaSuccess) return err;
   }
   const int64_t rows = static_cast<int64_t>(L.units) * L.heads * a.rows;
   tree_combine_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t tree_read_clear_error(uint32_t* flags) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t err = cudaMemcpyFromSymbol(&v, g_nq_error, sizeof(v));
+  if (err != cudaSuccess) return err;
+  if ((err = cudaMemcpyToSymbol(g_nq_error, &zero, sizeof(zero))) != cudaSuccess) return err;
+  *flags = v;
+  return cudaSuccess;
 }
 
 }  // namespace nq

@@ -478,9 +478,10 @@ nq_status nq_encode_slots(const void *K, nq_kv_strides ks, const void *V, nq_kv_
  * (strides os; must not overlap the inputs).  The packed part runs on the
  * tensor cores with f16 operands and fp32 accumulators: keys are rounded to
  * f16 after the rotation (2^-12 relative, as are the cos/sin), queries are
- * scaled by a power of two per row (exact), softmax weights and fp16-scaled
- * codes are rounded to f16, and statistics, sums and the draft part are fp32.
- * Queries must be finite with |q| <= 2^100, draft keys and values finite.
+ * scaled by a power of two per row (exact), softmax weights are rounded to
+ * f16 (codes are exact), and statistics, sums and the draft part are fp32.
+ * Queries must be finite, of a largest |q| per row in [2^-100, 2^100] or 0,
+ * and draft keys and values that some node sees finite.
  * Scores beyond 2^15 (in log2 units) are out of range of the fp32 exponent
  * arithmetic's precision, as for any fp32 softmax.
  * 1 <= G <= 8, 0 <= n < 2^31 (n = 0: the draft alone, k_in and v_in are not
@@ -523,7 +524,8 @@ int nq_get_decode_engine(void);
 /* -------------------------------------------------------------- status
  * Reads and clears the device error word of in-kernel failure reports
  * (bit 1: a tensor-core product of nq_decode / nq_decode_exact did not
- * complete within its bounded wait).  Synchronises the current device, so a
+ * complete within its bounded wait; bit 2: a wait of nq_tree_attend ran out,
+ * that call's output is then unspecified).  Synchronises the current device, so a
  * pending launch error surfaces here as NQ_ERR_CUDA. */
 nq_status nq_device_error(uint32_t *flags_out);
 

@@ -45,28 +45,6 @@
 
 namespace nq {
 
-// Division by a fixed divisor for numerators below 2^31 (round-up method of
-// Granlund and Montgomery): q = (n * m) >> (31 + l), l = ceil(log2 d),
-// m = floor(2^(31+l) / d) + 1.
-struct FastDiv {
-  uint64_t m;
-  uint32_t d, shift;
-};
-
-static FastDiv make_fastdiv(uint32_t d) {
-  uint32_t l = 0;
-  while ((1ull << l) < d) ++l;
-  FastDiv f;
-  f.d = d;
-  f.shift = 31 + l;
-  f.m = ((1ull << f.shift) / d) + 1;
-  return f;
-}
-
-__device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) {
-  return static_cast<uint32_t>((static_cast<uint64_t>(n) * f.m) >> f.shift);
-}
-
 struct CodecArgs {
   const uint16_t* kv;  // encode: bf16 input; decode: bf16 output
   int64_t su, sh, st;  // element strides of the bf16 tensor

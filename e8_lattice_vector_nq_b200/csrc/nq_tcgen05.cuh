@@ -194,6 +194,41 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
                : "memory");
 }
 
+// The same for a whole converged warp, one of whose lanes (on != 0) issues the
+// instruction.  The operands are read from uniform registers: in a branch of
+// one lane they would be moved there again for every instruction, which took
+// about 100 cycles each.
+__device__ __forceinline__ void umma_f16_if(uint32_t on, uint32_t d_tmem, uint64_t a_desc,
+                                            uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(on)
+      : "memory");
+}
+// 1 in one lane of the converged warp (always the same), 0 in the others.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(on)
+      :
+      : "memory");
+  return on;
+}
+
 // MN-major operand in the 128-byte swizzled layout: one row of 128 bytes (64
 // 16-bit elements along M or N) per k, groups of 8 k 1024 bytes apart, the
 // next 64 elements of M or N lbo bytes on (16-byte chunk c of row k stored at

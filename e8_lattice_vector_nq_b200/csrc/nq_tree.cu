@@ -27,14 +27,16 @@
 // scores leave that range (the first one always) takes the exact column
 // maxima; the others only compare (one vote per tile and warpgroup).
 //
-// One CTA per SM: four warpgroups of compute threads (thread: one token of
-// the tile; warpgroup: a quarter of the coordinates in 1 and 4, of the query
-// rows in 3), one warp that issues every MMA, one that stages codes
-// (cp.async, three tiles ahead, page by page).  The MMAs of a step run while
-// the threads work on the next: T(j+1) | softmax(j) | rotate(j+1) | V(j+1)
-// against S(j) | X(j+1) | O(j) | S(j+1).  The work of a launch is split over
-// the tokens (flash decoding) to fill the 148 SMs; tree_combine_kernel merges
-// the splits, applies H and attends the draft nodes in fp32.
+// One CTA per SM, its warpgroups specialised so that the phases of different
+// tiles overlap: two warpgroups make keys (a token per thread and half of its
+// coordinates: codes -> t, then X -> rotated keys), one makes values, two do
+// the softmax (half of the query rows each), and the last one's warps issue
+// the three products.  X is double buffered in TMEM, so the codes of tile j+1
+// go to the tensor cores before tile j is rotated.  Registers are moved to
+// the softmax warpgroups, which hold a sum per query row.  The work of a
+// launch is split over the tokens (flash decoding) to fill the 148 SMs;
+// tree_combine_kernel merges the splits, applies H and attends the draft
+// nodes in fp32.
 //
 // The angles of a tile are needed by every KV head and every row block:
 // tree_angles_kernel writes (c', s') once per call as f16 pairs in the order
@@ -47,8 +49,7 @@ namespace nq {
 
 constexpr int kTreeTile = 128;     // tokens per tile
 constexpr int kTreePart = 2 + kD;  // a split's m (log2 units), l, sums[128] in the code domain
-constexpr int kTreeStages = 3;
-constexpr int kTreeThreads = 512 + 64;  // compute threads, issuing warp, staging warp
+constexpr int kTreeThreads = 768;  // keys 2 x 128, values 128, softmax 2 x 128, issue 128
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kTreeWaitLimit = 1u << 20;
@@ -57,7 +58,7 @@ constexpr uint32_t kErrTreeTimeout = 4u;
 struct TreeArgs {
   TreeLaunch L;
   int rows;         // nodes * G rows per KV head, row = node * G + g
-  int ncols;        // query rows per CTA (4 * NR)
+  int ncols;        // query rows per CTA
   int rblocks;      // CTAs per (unit, KV head, split)
   int64_t n_a;
   int64_t tiles;    // ceil(n / 128)
@@ -65,6 +66,7 @@ struct TreeArgs {
   int64_t nsplit;
   float* part;      // [units * heads][rows][nsplit][kTreePart]
   uint4* angles;    // [units or 1][tiles][4][4][128]
+  FastDiv page;     // division by the page size
   int64_t angle_stride;  // entries per unit, 0 when shared
 };
 
@@ -201,13 +203,6 @@ __device__ __forceinline__ void tree_unpack(const uint32_t (&w)[BITS], uint32_t 
   }
 }
 
-// This thread's BITS words (32 codes) of a staged row.
-template <int BITS>
-__device__ __forceinline__ void tree_words(uint32_t addr, uint32_t (&w)[BITS]) {
-#pragma unroll
-  for (int i = 0; i < BITS; ++i) w[i] = lds32(addr + 4 * i);
-}
-
 // Row t, 16-byte chunk c of an operand of 128-byte swizzled rows (the K-major
 // layout with a token per row and the MN-major one with a token per k are the
 // same addresses).
@@ -222,30 +217,31 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ------------------------------------------------------------ shared memory
-template <int BK, int BV, int NR>
+template <int BK, int BV, int N>
 struct TreeSmem {
-  static constexpr int N = 4 * NR;
+  static constexpr int KBufs = N > 64 ? 1 : 2;          // what fits
   static constexpr int T = 0;                           // t of the keys: 2 x (128 rows x 128 B)
   static constexpr int K = T + 32768;                   // rotated keys, the same
-  static constexpr int V = K + 32768;                   // scaled value codes
-  static constexpr int P = V + 32768;                   // weights: N/64 blocks of 128 rows
+  static constexpr int V = K + KBufs * 32768;           // scaled value codes, two tiles
+  static constexpr int P = V + 2 * 32768;               // weights: N/64 blocks of 128 rows
   static constexpr int Q = P + (N > 64 ? 2 : 1) * 16384;  // queries: 2 x (N rows x 128 B)
   static constexpr int H = Q + N * 256;                 // H64, 64 rows x 128 B
   static constexpr int CA = H + 8192;                   // coset bits of the tile, 128 x 16 f16
   static constexpr int CB = CA + 4096;                  // their rows of H, 128 x 16 f16
-  static constexpr int Stage = CB + 4096;
-  static constexpr int KC = 128 * 16 * BK, VC = 128 * 16 * BV;
-  static constexpr int StageBytes = KC + VC + 3 * 512;  // codes, key meta, value meta, validity
-  static constexpr int FM = Stage + kTreeStages * StageBytes;  // (f0, f1, -m0, -m1) per row pair
-  static constexpr int WMax = FM + N * 8;               // [4 warpgroups][NR][4 warps]
-  static constexpr int Vec = WMax + N * 16;             // staging warp: vector indexes of a tile
-  static constexpr int Bars = Vec + 2048;
+  static constexpr int Kap = CB + 4096;                 // key scales of 8 tiles (-1: no token)
+  static constexpr int Vm = Kap + 8 * 512;              // value scale mantissas of 8 tiles
+  static constexpr int FM = Vm + 8 * 512;               // (f0, f1, -m0, -m1) per row pair
+  static constexpr int WMax = FM + N * 8;               // [N][4 warps]
+  static constexpr int Bars = WMax + N * 16;
   static constexpr int Bytes = Bars + 128 + 1024;       // 1 KB of slack to align the base
   static_assert(Bytes <= 232448, "one CTA per SM within 227 KB");
 };
 
 // Bounded wait; past the limit the error word is set and `dead` makes every
 // later wait of the CTA return at once (its results are then unspecified).
+// A wait names its phase by parity, so no phase may complete twice before a
+// waiter has looked: each barrier's next phase needs something that its
+// waiters do after their wait for this one.
 __device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
   bool done = mbar_try_wait(bar, parity);
   for (uint32_t spin = 0; !done && spin < kTreeWaitLimit; ++spin)
@@ -257,20 +253,104 @@ __device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatil
   __syncwarp();
 }
 
-template <int BK, int BV, int NR>
+// A 128-byte swizzled operand whose first row is at 16 * addr4, groups of 8
+// rows 1024 bytes apart (see desc_sw128, desc_sw128_mn).
+__device__ __forceinline__ uint64_t tree_desc(uint32_t addr4, uint32_t lbo4) {
+  constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return (static_cast<uint64_t>(kHigh) << 32) | (addr4 | (lbo4 << 16));
+}
+
+// One arrival for the warp, after its threads' shared-memory writes (fenced
+// for the MMA by the callers that wrote operands).
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+template <int REGS>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+// Registers per thread of the roles, out of the 768 x 80 = 61440 that the block
+// is launched with.
+template <int N>
+struct TreeRegs {
+  static constexpr int Softmax = N > 64 ? 128 : 96, Keys = N > 64 ? 64 : 80,
+                       Values = N > 64 ? 56 : 80, Issue = 40;
+  static_assert(2 * Softmax + 2 * Keys + Values + Issue <= 6 * 80, "the launch's registers");
+};
+
+// The tokens of one thread, tile by tile: the unit or page that holds the
+// token (-1: no token) and its slot there.  The page entry of the next tile is
+// in flight.
+struct TokenWalk {
+  const int32_t* row;  // the unit's row of the page table, or NULL
+  const FastDiv& div;
+  int64_t pages;
+  uint32_t t, t1;  // this thread's token of the tile that `page` belongs to; end of the split
+  int32_t page;
+
+  __device__ __forceinline__ TokenWalk(const TreeArgs& a, int64_t u, int64_t tok, int64_t end)
+      : div(a.page), pages(a.L.pages), t(static_cast<uint32_t>(tok)), t1(static_cast<uint32_t>(end)) {
+    row = a.L.table ? a.L.table + u * a.L.table_stride : nullptr;
+    page = static_cast<int32_t>(u);
+    fetch();
+  }
+  __device__ __forceinline__ void fetch() {
+    if (row && t < t1) page = __ldg(row + fdiv(t, div));
+  }
+  __device__ __forceinline__ void next(int32_t& lead, uint32_t& slot) {
+    const bool ok = t < t1 && (!row || (page >= 0 && page < pages));
+    lead = ok ? page : -1;
+    slot = row ? t - fdiv(t, div) * div.d : t;
+    t += kTreeTile;
+    fetch();
+  }
+};
+
+// A value's scale sigma = 2^e m with e >= -22 (so that 2^(e-2) t is exact in
+// f16), 1 <= m < 2 (or below for the smallest scales); 7 * 2^13 stays in range.
+__device__ __forceinline__ void value_scale(uint32_t meta, float& m, int& e) {
+  const float sig = __half2float(__ushort_as_half(static_cast<unsigned short>(meta >> 16)));
+  e = max(static_cast<int>(__float_as_uint(sig) >> 23) - 127, -22);
+  m = sig * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+constexpr uint32_t kTmX = 0, kTmS = 256;  // TMEM columns: X twice, S, O
+
+template <int V>
+struct Parity {
+  static constexpr int value = V;
+};
+
+template <int BK, int BV, int N>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const TreeArgs a) {
-  using S = TreeSmem<BK, BV, NR>;
-  constexpr int N = S::N;
+  using S = TreeSmem<BK, BV, N>;
   extern __shared__ __align__(1024) unsigned char tree_smem[];
   const uint32_t raw = smem_u32(tree_smem);
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* gen = tree_smem + (base - raw);  // generic pointer of the aligned base
   const TreeLaunch& L = a.L;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t bar_x = base + S::Bars, bar_s = bar_x + 8, bar_o = bar_x + 16;
-  const uint32_t full = bar_x + 24, empty = full + 8 * kTreeStages;
-  const uint32_t tslot = empty + 8 * kTreeStages;
-  volatile uint32_t* dead = reinterpret_cast<volatile uint32_t*>(gen + (tslot + 4 - base));
+  // barriers: codes written, X done, keys written, S done, S read, values
+  // written, weights written, O done (the scales of a tile are written with
+  // its codes).  Where a buffer is double, so is its barrier: tile j uses
+  // barrier j & 1 in its phase j >> 1.
+  const uint32_t bar_t = base + S::Bars, bar_x = bar_t + 8, bar_sf = bar_t + 16, bar_p = bar_t + 24;
+  auto bar_k = [&](int j) { return bar_t + 32 + 8 * (j & 1); };
+  auto bar_s = [&](int j) { return bar_t + 48 + 8 * (j & 1); };
+  auto bar_v = [&](int j) { return bar_t + 64 + 8 * (j & 1); };
+  auto bar_o = [&](int j) { return bar_t + 80 + 8 * (j & 1); };
+  const uint32_t tslot = bar_t + 96;
+  volatile uint32_t* dead = reinterpret_cast<volatile uint32_t*>(gen + S::Bars + 100);
 
   // block index -> (split, unit * heads + head, row block): the row blocks and
   // heads of the same tokens are neighbours (their codes and angles meet in L2)
@@ -296,18 +376,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
   }
 
   // ---- setup: barriers, TMEM, constant operands, queries
-  constexpr uint32_t kCols = 128 + 2 * N <= 256 ? 256u : 512u;  // X, S, O
-  if (warp == 16) {
+  constexpr uint32_t kCols = 512;  // X twice, S, O
+  if (warp == 20) {
     tmem_alloc(tslot, kCols);
     tmem_relinquish();
   }
   if (tid == 0) {
+    mbar_init(bar_t, 8);
     mbar_init(bar_x, 1);
-    mbar_init(bar_s, 1);
-    mbar_init(bar_o, 1);
-    for (int s = 0; s < kTreeStages; ++s) {
-      mbar_init(full + 8 * s, 64);   // each staging lane: its copies, its stores
-      mbar_init(empty + 8 * s, 16);  // each compute warp
+    mbar_init(bar_sf, 8);
+    mbar_init(bar_p, 8);
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(bar_k(j), 8);
+      mbar_init(bar_s(j), 2);  // the products, and their issuer (see there)
+      mbar_init(bar_v(j), 4);
+      mbar_init(bar_o(j), 1);
     }
     *dead = 0u;
     fence_mbar_init();
@@ -327,9 +410,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
       v[i] = pr;
     }
     sts128(base + S::H + row_chunk(n, c), make_uint4(v[0], v[1], v[2], v[3]));
-  }
-  if (tid < 256) {  // coset slots: output row n, groups 8c .. 8c+7 (u rows: c = 0, v rows: c = 1)
-    const int n = tid >> 1, c = tid & 1;
+  } else {  // coset slots: output row n, groups 8c .. 8c+7 (u rows: c = 0, v rows: c = 1)
+    const int n = (tid - 512) >> 1, c = tid & 1;
     uint32_t v[4] = {0u, 0u, 0u, 0u};
     if ((n >> 6) == c && (n & 7) == 0) {
 #pragma unroll
@@ -340,431 +422,470 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
     }
     sts128(base + S::CB + c * 2048 + n * 16, make_uint4(v[0], v[1], v[2], v[3]));
   }
-  if (warp < 16) {
-    for (int r = warp; r < N; r += 16) {
-      const int row = row0 + r;
-      float q[4] = {0.f, 0.f, 0.f, 0.f};
-      if (row < a.rows) {
-        const int node = row / L.G, j = h * L.G + row % L.G;
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(
-                                  static_cast<const uint16_t*>(L.q) + u * L.qs.unit +
-                                  j * L.qs.head + node * L.qs.token) + lane);
-        q[0] = bf16lo(v.x);
-        q[1] = bf16hi(v.x);
-        q[2] = bf16lo(v.y);
-        q[3] = bf16hi(v.y);
-      }
-      float m = fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])));
+  for (int r = warp; r < N; r += kTreeThreads / 32) {
+    const int row = row0 + r;
+    float q[4] = {0.f, 0.f, 0.f, 0.f};
+    if (row < a.rows) {
+      const int node = row / L.G, j = h * L.G + row % L.G;
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(L.q) +
+                                                           u * L.qs.unit + j * L.qs.head +
+                                                           node * L.qs.token) + lane);
+      q[0] = bf16lo(v.x);
+      q[1] = bf16hi(v.x);
+      q[2] = bf16lo(v.y);
+      q[3] = bf16hi(v.y);
+    }
+    float m = fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])));
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      // |q| 2^-e in [2^13, 2^14): bf16 values fit f16 exactly down to 2^-24 of
-      // that scale's 2^-14, i.e. 2^-28 of the row's largest before any rounding
-      const int e = m > 0.f && m < INFINITY ? static_cast<int>(__float_as_uint(m) >> 23) - 127 - 13 : 0;
-      const float down = e >= -126 && e <= 126 ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.f;
-      const __half2 p0 = __floats2half2_rn(q[0] * down, q[1] * down);
-      const __half2 p1 = __floats2half2_rn(q[2] * down, q[3] * down);
-      const int c = lane >> 1;  // chunk of 8 coordinates, this lane's half of it
-      const uint32_t dst = base + S::Q + (c >> 3) * (N * 128) + row_chunk(r, c & 7) + (lane & 1) * 8;
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst),
-                   "r"(*reinterpret_cast<const uint32_t*>(&p0)),
-                   "r"(*reinterpret_cast<const uint32_t*>(&p1))
-                   : "memory");
-      if (lane == 0) {
-        float* fm = reinterpret_cast<float*>(gen + S::FM) + (r >> 1) * 4 + (r & 1);
-        const float up = down > 0.f ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 0.f;
-        fm[0] = L.scale * kLog2e * up;
-        fm[2] = 0.f;
-      }
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // |q| 2^-e in [2^13, 2^14): a bf16 value is exact in f16 down to 2^-29 of
+    // the row's largest
+    const int e = m > 0.f && m < INFINITY ? static_cast<int>(__float_as_uint(m) >> 23) - 127 - 13 : 0;
+    const float down = e >= -126 && e <= 126 ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 0.f;
+    const __half2 p0 = __floats2half2_rn(q[0] * down, q[1] * down);
+    const __half2 p1 = __floats2half2_rn(q[2] * down, q[3] * down);
+    const int c = lane >> 1;  // chunk of 8 coordinates, this lane's half of it
+    const uint32_t dst = base + S::Q + (c >> 3) * (N * 128) + row_chunk(r, c & 7) + (lane & 1) * 8;
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst),
+                 "r"(*reinterpret_cast<const uint32_t*>(&p0)),
+                 "r"(*reinterpret_cast<const uint32_t*>(&p1))
+                 : "memory");
+    if (lane == 0) {
+      float* fm = reinterpret_cast<float*>(gen + S::FM) + (r >> 1) * 4 + (r & 1);
+      const float up = down > 0.f ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 0.f;
+      fm[0] = L.scale * kLog2e * up;
+      fm[2] = 0.f;
     }
   }
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = lds32(tslot);
-  const uint32_t tX = tmem, tS = tmem + 128, tO = tmem + 128 + N;
+  // the whole of TMEM is allocated (512 columns), so it starts at column 0
+  const uint32_t tmem = 0u, tX = kTmX, tS = kTmS, tO = kTmS + N;
+  const int t = tid & 127;
+  const uint32_t t_lane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
 
-  if (warp == 17) {
-    // ------------------------------------------------------------- staging
-    int64_t* vec = reinterpret_cast<int64_t*>(gen + S::Vec);
-    for (int j = 0; j < nt; ++j) {
-      const int s = j % kTreeStages;
-      if (j >= kTreeStages) tree_wait(empty + 8 * s, ((j / kTreeStages) - 1) & 1, dead);
-      const uint32_t st = base + S::Stage + s * S::StageBytes;
-      float* inv = reinterpret_cast<float*>(gen + S::Stage + s * S::StageBytes + S::KC + S::VC + 1024);
-      __syncwarp();
+  if (warp < 8) {
+    // ------------------------------------------------------------- keys
+    // Thread (t, kw): token t, codes 64 kw .. +63, frequencies 32 kw .. +31.
+    if constexpr (TreeRegs<N>::Keys < 80) regs_dec<TreeRegs<N>::Keys>();
+    const int kw = warp >> 2;
+    const uint4* ang = a.angles + u * a.angle_stride + ((split * a.per * 4 + 2 * kw) * 4) * 128 + t;
+    TokenWalk walk(a, u, t0 + t, t1);
+    uint32_t wd[2 * BK], meta, vmeta = 0u;
+    int32_t lead;  // where the token of the tile after the loaded one is
+    uint32_t slot;
+    const int64_t khead = h * L.k_in.head_stride, vhead = h * L.v_in.head_stride;
+    auto load = [&]() {
+      if (lead >= 0) {
+        const int64_t v = lead * L.k_in.unit_stride + khead + slot;
+        const uint32_t* src = L.k_in.codes + v * (4 * BK) + kw * (2 * BK);
+        if constexpr (BK == 2) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+          wd[0] = x.x, wd[1] = x.y, wd[2] = x.z, wd[3] = x.w;
+        } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tk = lane + 32 * i;
-        const int64_t t = t0 + static_cast<int64_t>(j) * kTreeTile + tk;
-        int64_t vk = -1, vv = -1;
-        if (t < t1) {
-          if (!L.table) {
-            vk = u * L.k_in.unit_stride + h * L.k_in.head_stride + t;
-            vv = u * L.v_in.unit_stride + h * L.v_in.head_stride + t;
-          } else {
-            const uint32_t pj = static_cast<uint32_t>(t) / static_cast<uint32_t>(L.page_size);
-            const int64_t page = __ldg(L.table + u * L.table_stride + pj);
-            if (page >= 0 && page < L.pages) {
-              const int64_t off = t - static_cast<int64_t>(pj) * L.page_size;
-              vk = page * L.k_in.unit_stride + h * L.k_in.head_stride + off;
-              vv = page * L.v_in.unit_stride + h * L.v_in.head_stride + off;
+          for (int i = 0; i < 3; ++i) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(src) + i);
+            wd[2 * i] = x.x, wd[2 * i + 1] = x.y;
+          }
+        }
+        meta = __ldg(L.k_in.meta + v);
+        if (kw == 1) vmeta = __ldg(L.v_in.meta + (lead * L.v_in.unit_stride + vhead + slot));
+      } else {  // a NaN scale marks it: the codec's scales are finite
+#pragma unroll
+        for (int i = 0; i < 2 * BK; ++i) wd[i] = 0u;
+        meta = 0xFFFF0000u;
+      }
+    };
+    // codes of tile j -> T and coset slots; then the loads of tile j+1
+    auto write_t = [&](int j) {
+      const uint32_t dst = base + S::T + kw * 16384;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        uint32_t w[BK], hh[16];
+#pragma unroll
+        for (int i = 0; i < BK; ++i) w[i] = wd[s * BK + i];
+        tree_unpack<BK>(w, hh);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          sts128(dst + row_chunk(t, 4 * s + c),
+                 make_uint4(hh[4 * c], hh[4 * c + 1], hh[4 * c + 2], hh[4 * c + 3]));
+      }
+      // coset bits 8kw .. 8kw+7 as f16 0 or 1 (bit 2u at bit 0 of y >> 2u, bit
+      // 2u+1 at bit 16)
+      const uint32_t cb = (meta >> (8 * kw)) & 255u, y = cb | (cb << 15);
+      sts128(base + S::CA + kw * 2048 + t * 16,
+             make_uint4((y & 0x10001u) * 0x3C00u, ((y >> 2) & 0x10001u) * 0x3C00u,
+                        ((y >> 4) & 0x10001u) * 0x3C00u, ((y >> 6) & 0x10001u) * 0x3C00u));
+      if (kw == 0) {
+        const float sig = __half2float(__ushort_as_half(static_cast<unsigned short>(meta >> 16)));
+        const float kap = __fmul_rn(__fmul_rn(sig, 0.5f), __uint_as_float(kCBits));
+        reinterpret_cast<float*>(gen + S::Kap)[(j & 7) * 128 + t] = kap >= 0.f ? kap : -1.0f;
+      } else {
+        float m;
+        int e;
+        value_scale(vmeta, m, e);
+        reinterpret_cast<float*>(gen + S::Vm)[(j & 7) * 128 + t] = m;
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      warp_arrive(bar_t, lane);
+      load();
+      walk.next(lead, slot);
+      if (lead >= 0) {
+        const int64_t v = lead * L.k_in.unit_stride + khead + slot;
+        prefetch_l2(L.k_in.codes + v * (4 * BK) + kw * (2 * BK));
+        if (kw == 0) prefetch_l2(L.k_in.meta + v);
+      }
+    };
+    walk.next(lead, slot);
+    load();
+    walk.next(lead, slot);
+    write_t(0);
+    for (int j = 0; j < nt; ++j) {
+      uint4 cs[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) cs[x] = __ldg(ang + x * 128);
+      tree_wait(bar_x, j & 1, dead);
+      tc_fence_after();
+      if (j + 1 < nt) write_t(j + 1);
+      // the keys that this buffer held have been read
+      if (j >= S::KBufs) tree_wait(bar_s(j - S::KBufs), ((j - S::KBufs) >> 1) & 1, dead);
+      const uint32_t kb = base + S::K + (j % S::KBufs) * 32768;
+      const uint32_t x0 = tX + t_lane + (j & 1) * 128 + 32 * kw;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // eight frequencies at a time
+        uint32_t uu[8], vv[8];
+        tmem_ld(x0 + 8 * q, uu);
+        tmem_ld(x0 + 64 + 8 * q, vv);
+        tmem_wait_ld(uu);
+        tmem_wait_ld(vv);
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const uint4& e = cs[2 * (q & 1) + (f >> 1)];
+          const uint32_t cw = (f & 1) ? e.z : e.x, sw = (f & 1) ? e.w : e.y;
+          const __half2 c = *reinterpret_cast<const __half2*>(&cw);
+          const __half2 s = *reinterpret_cast<const __half2*>(&sw);
+          // u and v are integers up to 448: exact in f16
+          const __half2 U = __floats2half2_rn(__uint_as_float(uu[2 * f]), __uint_as_float(uu[2 * f + 1]));
+          const __half2 V = __floats2half2_rn(__uint_as_float(vv[2 * f]), __uint_as_float(vv[2 * f + 1]));
+          const __half2 a0 = __hfma2(U, c, __hmul2(V, s));
+          const __half2 a1 = __hfma2(__hneg2(V), c, __hmul2(U, s));
+          lo[f] = *reinterpret_cast<const uint32_t*>(&a0);
+          hi[f] = *reinterpret_cast<const uint32_t*>(&a1);
+        }
+        if (q < 2) {  // the angles of the frequencies after the next eight
+          cs[2 * q] = __ldg(ang + (4 + 2 * q) * 128);
+          cs[2 * q + 1] = __ldg(ang + (5 + 2 * q) * 128);
+        }
+        const uint32_t dst = kb + row_chunk(t, 4 * kw + q);
+        sts128(dst, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        sts128(dst + 16384, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      }
+      ang += 16 * 128;
+      fence_proxy_async_smem();
+      tc_fence_before();
+      warp_arrive(bar_k(j), lane);
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ values
+    if constexpr (TreeRegs<N>::Values < 80) regs_dec<TreeRegs<N>::Values>();
+    TokenWalk walk(a, u, t0 + t, t1);
+    uint32_t wd[4 * BV], meta;
+    int32_t lead;
+    uint32_t slot;
+    const int64_t vhead = h * L.v_in.head_stride;
+    auto load = [&]() {
+      const int64_t v = lead * L.v_in.unit_stride + vhead + slot;
+#pragma unroll
+      for (int i = 0; i < BV; ++i) {
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (lead >= 0) x = __ldg(reinterpret_cast<const uint4*>(L.v_in.codes + v * (4 * BV)) + i);
+        wd[4 * i] = x.x, wd[4 * i + 1] = x.y, wd[4 * i + 2] = x.z, wd[4 * i + 3] = x.w;
+      }
+      meta = lead >= 0 ? __ldg(L.v_in.meta + v) : 0u;
+    };
+    walk.next(lead, slot);
+    load();
+    walk.next(lead, slot);
+    for (int j = 0; j < nt; ++j) {
+      if (j > 1) tree_wait(bar_o(j), ((j >> 1) - 1) & 1, dead);  // the values of tile j-2 have been read
+      float m;
+      int e;
+      value_scale(meta, m, e);
+      const uint32_t s16 = __half_as_ushort(
+          __float2half_rn(__uint_as_float(static_cast<uint32_t>(125 + e) << 23)));
+      const uint32_t ss = s16 | (s16 << 16), neg = ss ^ 0x80008000u;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {  // 32 codes at a time
+        uint32_t x[BV], hh[16];
+#pragma unroll
+        for (int i = 0; i < BV; ++i) x[i] = wd[w * BV + i];
+        tree_unpack<BV>(x, hh);
+        // byte g of z has coset bit g of these codes in its top bit; a byte
+        // permute that repeats top bits makes the -2^(e-2) lanes of the set groups
+        const uint32_t z = ((meta >> (4 * w)) & 15u) * 0x10204080u;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const int ga = tree_slot<BV>(2 * q) >> 3, gb = tree_slot<BV>(2 * q + 1) >> 3;
+          uint32_t m;  // (prmt's sign mode: __byte_perm has no form of it)
+          asm("prmt.b32 %0, %1, %1, %2;"
+              : "=r"(m)
+              : "r"(z), "r"(0x8888u | (ga * 0x11u) | (gb * 0x1100u)));
+          hh[q] = hfma2u(hh[q], ss, neg & m);
+        }
+        const uint32_t dst = base + S::V + (j & 1) * 32768 + (w >> 1) * 16384;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          sts128(dst + row_chunk(t, (w & 1) * 4 + c),
+                 make_uint4(hh[4 * c], hh[4 * c + 1], hh[4 * c + 2], hh[4 * c + 3]));
+      }
+      fence_proxy_async_smem();
+      warp_arrive(bar_v(j), lane);
+      load();
+      walk.next(lead, slot);
+      if (lead >= 0) {
+        const int64_t v = lead * L.v_in.unit_stride + vhead + slot;
+        prefetch_l2(L.v_in.codes + v * (4 * BV));
+        prefetch_l2(L.v_in.meta + v);
+      }
+    }
+  } else if (warp < 20) {
+    // ----------------------------------------------------------- softmax
+    // Thread (t, w): token t, query rows HN w .. HN w + HN - 1 of the block.
+    regs_inc<TreeRegs<N>::Softmax>();
+    constexpr int HN = N / 2, CH = HN < 32 ? HN : 32;  // columns; columns at a time
+    const int w = (warp - 12) >> 2, wl = warp & 3;
+    const uint32_t bid = 1 + w;  // this warpgroup's named barrier
+    float4* fm = reinterpret_cast<float4*>(gen + S::FM) + w * (HN / 2);
+    int* wmax = reinterpret_cast<int*>(gen + S::WMax) + w * (HN * 4);
+    float l[HN];
+#pragma unroll
+    for (int c = 0; c < HN; ++c) l[c] = 0.f;
+    bool started = false;  // some token of the split was valid
+
+    for (int j = 0; j < nt; ++j) {
+      tree_wait(bar_s(j), (j >> 1) & 1, dead);
+      tc_fence_after();
+      const float kv = reinterpret_cast<const float*>(gen + S::Kap)[(j & 7) * 128 + t];
+      const bool valid = kv >= 0.f;
+      const float vm = reinterpret_cast<const float*>(gen + S::Vm)[(j & 7) * 128 + t];
+      bool raised = false;
+#pragma unroll
+      for (int h0 = 0; h0 < HN; h0 += CH) {
+        float y[CH];
+        {
+          constexpr int LD = CH < 16 ? CH : 16;
+#pragma unroll
+          for (int c0 = 0; c0 < CH; c0 += LD) {
+            uint32_t s[LD];
+            tmem_ld(tS + t_lane + w * HN + h0 + c0, s);
+            tmem_wait_ld(s);
+#pragma unroll
+            for (int c = 0; c < LD; c += 2) {
+              const float4 f = fm[(h0 + c0 + c) / 2];
+              const float2 g = mul2(make_float2(f.x, f.y), make_float2(kv, kv));
+              const float2 v = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                    g, make_float2(f.z, f.w));
+              y[c0 + c] = v.x;
+              y[c0 + c + 1] = v.y;
             }
           }
         }
-        vec[tk] = vk;
-        vec[128 + tk] = vv;
-        inv[tk] = vk >= 0 ? 0.f : -INFINITY;
-        const uint32_t mb = vk >= 0 ? 4u : 0u;  // bytes to copy, the rest is zero-filled
-        const uint32_t md = st + S::KC + S::VC + tk * 4;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(md),
-                     "l"(L.k_in.meta + (vk < 0 ? 0 : vk)), "r"(mb)
-                     : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(md + 512),
-                     "l"(L.v_in.meta + (vv < 0 ? 0 : vv)), "r"(mb)
-                     : "memory");
-      }
-      __syncwarp();
-      auto copy = [&](const uint32_t* codes, int bits, const int64_t* vx, uint32_t dst) {
-        for (int c = lane; c < 128 * bits; c += 32) {
-          const int tk = c / bits;
-          const int64_t v = vx[tk];
-          const uint32_t* src = codes + (v < 0 ? 0 : v) * (4 * bits) + (c - tk * bits) * 4;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + c * 16), "l"(src),
-                       "r"(v < 0 ? 0u : 16u)
-                       : "memory");
+        if (h0 + CH == HN) {  // S has been read
+          tc_fence_before();
+          warp_arrive(bar_sf, lane);
         }
-      };
-      copy(L.k_in.codes, BK, vec, st);
-      copy(L.v_in.codes, BV, vec + 128, st + S::KC);
-      mbar_arrive_cp_async(full + 8 * s);
-      mbar_arrive(full + 8 * s);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-  } else if (warp == 16) {
-    // ------------------------------------------------------------ the MMAs
-    constexpr uint32_t iX = idesc_f16_f32(128, 64), iC = idesc_f16_f32(128, 128);
-    constexpr uint32_t iS = idesc_f16_f32(128, N), iO = idesc_f16_f32(128, N) | kIdescAMn | kIdescBMn;
-    auto mma_x = [&]() {
-      umma_f16(tX, desc_plain(base + S::CA, 2048, 128), desc_plain(base + S::CB, 2048, 128), iC, 0u);
+        if (!valid) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+          for (int c = 0; c < CH; ++c) y[c] = -INFINITY;
+        }
+        float top = y[0];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma_f16(tX + 64 * hf, desc_sw128(base + S::T + hf * 16384 + k * 32),
-                   desc_sw128(base + S::H + k * 32), iX, 1u);
-      umma_commit(bar_x);
-    };
-    auto mma_s = [&]() {
+        for (int c = 1; c < CH; ++c) top = fmaxf(top, y[c]);
+        const bool raise = named_bar_or(bid, 128, top > 14.0f || (!started && valid));
+        // the sums are to be rescaled, or weights to be written: O is at rest
+        // and P is free
+        auto o_at_rest = [&]() {
+          if (j > 0) tree_wait(bar_o(j - 1), ((j - 1) >> 1) & 1, dead);
+          tc_fence_after();
+        };
+        if (raise) {
+          if (h0 == 0) o_at_rest();
+          raised = true;
+          // exact column maxima of the tile, as ordered integers
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        umma_f16(tS, desc_sw128(base + S::K + (k >> 2) * 16384 + (k & 3) * 32),
-                 desc_sw128(base + S::Q + (k >> 2) * (N * 128) + (k & 3) * 32), iS, k > 0);
-      umma_commit(bar_s);
-    };
-    auto mma_o = [&](bool acc) {
+          for (int c = 0; c < CH; ++c) {
+            const int i = __float_as_int(y[c]);
+            const int k = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
+            if (lane == 0) wmax[(h0 + c) * 4 + wl] = k;
+          }
+          named_bar_sync(bid, 128);
+          auto delta_of = [&](int c) {
+            const int4 k4 = *reinterpret_cast<const int4*>(wmax + c * 4);
+            const int k = max(max(k4.x, k4.y), max(k4.z, k4.w));
+            const float d = __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)) - 6.0f;
+            return started ? fmaxf(d, 0.f) : d;
+          };
+          if (t < CH) {
+            float* m = reinterpret_cast<float*>(fm + ((h0 + t) >> 1)) + 2 + (t & 1);
+            *m -= delta_of(h0 + t);
+          }
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        umma_f16(tO, desc_sw128_mn(base + S::V + k * 2048, 16384),
-                 desc_sw128_mn(base + S::P + k * 2048, 16384), iO, acc || k > 0);
-      umma_commit(bar_o);
-    };
-    constexpr uint32_t kAll = 512 + 32;
-    named_bar_sync(5, kAll);
-    tc_fence_after();
-    if (lane == 0) mma_x();
-    named_bar_sync(7, kAll);
-    tc_fence_after();
-    if (lane == 0) mma_s();
-    for (int j = 0; j < nt; ++j) {
-      if (j + 1 < nt) {
-        named_bar_sync(5, kAll);
-        tc_fence_after();
-        if (lane == 0) mma_x();
-      }
-      named_bar_sync(6, kAll);
-      tc_fence_after();
-      if (lane == 0) mma_o(j > 0);
-      if (j + 1 < nt) {
-        named_bar_sync(7, kAll);
-        tc_fence_after();
-        if (lane == 0) mma_s();
-      }
-      __syncwarp();
-    }
-  } else {
-    // ------------------------------------------------------ compute threads
-    constexpr uint32_t kAll = 512 + 32;
-    const int w = tid >> 7, t = tid & 127, wl = warp & 3;
-    const uint32_t t_lane = static_cast<uint32_t>(32 * wl) << 16;
-    const uint4* ang = a.angles + u * a.angle_stride +
-                       ((split * a.per * 4 + w) * 4) * 128 + t;  // tile 0 of the split
-    auto stage_of = [&](int j) { return base + S::Stage + (j % kTreeStages) * S::StageBytes; };
-
-    // keys of tile j -> T and coset slots
-    auto write_t = [&](int j, float& kap, bool& valid) {
-      const uint32_t st = stage_of(j);
-      tree_wait(full + 8 * (j % kTreeStages), (j / kTreeStages) & 1, dead);
-      uint32_t wd[BK], hh[16];
-      tree_words<BK>(st + t * (16 * BK) + w * (4 * BK), wd);
-      const uint32_t meta = lds32(st + S::KC + S::VC + t * 4);
-      valid = lds32(st + S::KC + S::VC + 1024 + t * 4) == 0u;
-      tree_unpack<BK>(wd, hh);
-      const uint32_t dst = base + S::T + (w >> 1) * 16384;
+          for (int c0 = 0; c0 < CH; c0 += 4) {
+            float al[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        sts128(dst + row_chunk(t, (w & 1) * 4 + c),
-               make_uint4(hh[4 * c], hh[4 * c + 1], hh[4 * c + 2], hh[4 * c + 3]));
-      // coset bits 4w .. 4w+3 as f16 0 or 1
-      const uint32_t cm = meta >> (4 * w);
-      const uint32_t c01 = ((cm & 1u) * 0x3C00u) | (((cm >> 1) & 1u) * 0x3C000000u);
-      const uint32_t c23 = (((cm >> 2) & 1u) * 0x3C00u) | (((cm >> 3) & 1u) * 0x3C000000u);
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(base + S::CA + (w >> 1) * 2048 + t * 16 +
-                                                              (w & 1) * 8),
-                   "r"(c01), "r"(c23)
-                   : "memory");
-      const float sig = __half2float(__ushort_as_half(static_cast<unsigned short>(meta >> 16)));
-      kap = __fmul_rn(__fmul_rn(sig, 0.5f), __uint_as_float(kCBits));
-      fence_proxy_async_smem();
-      tc_fence_before();
-      named_bar_arrive(5, kAll);
-    };
-    // X of tile j -> rotated keys
-    auto write_k = [&](const uint4 (&cs)[4], uint32_t par) {
-      tree_wait(bar_x, par, dead);
-      tc_fence_after();
-      uint32_t uu[16], vv[16];
-      tmem_ld(tX + t_lane + 16 * w, uu);
-      tmem_ld(tX + t_lane + 64 + 16 * w, vv);
-      tmem_wait_ld(uu);
-      tmem_wait_ld(vv);
-      uint32_t lo[8], hi[8];
+            for (int c = 0; c < 4; ++c) {
+              const float d = delta_of(h0 + c0 + c);
+              y[c0 + c] -= d;
+              al[c] = ex2(-d);
+              l[h0 + c0 + c] = started ? l[h0 + c0 + c] * al[c] : 0.f;
+            }
+            if (started && j > 0) {
+              uint32_t o[4];
+              tmem_ld(tO + t_lane + w * HN + h0 + c0, o);
+              tmem_wait_ld(o);
 #pragma unroll
-      for (int f = 0; f < 8; ++f) {
-        const uint32_t cw = (f & 1) ? cs[f >> 1].z : cs[f >> 1].x;
-        const uint32_t sw = (f & 1) ? cs[f >> 1].w : cs[f >> 1].y;
-        const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&cw));
-        const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw));
-        const float2 U = make_float2(__uint_as_float(uu[2 * f]), __uint_as_float(uu[2 * f + 1]));
-        const float2 V = make_float2(__uint_as_float(vv[2 * f]), __uint_as_float(vv[2 * f + 1]));
-        const float2 a0 = fma2(U, c, mul2(V, s));
-        const float2 vc = mul2(V, c);
-        const float2 a1 = fma2(U, s, make_float2(-vc.x, -vc.y));
-        const __half2 p0 = __floats2half2_rn(a0.x, a0.y), p1 = __floats2half2_rn(a1.x, a1.y);
-        lo[f] = *reinterpret_cast<const uint32_t*>(&p0);
-        hi[f] = *reinterpret_cast<const uint32_t*>(&p1);
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t dst = base + S::K + row_chunk(t, 2 * w + c);
-        sts128(dst, make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]));
-        sts128(dst + 16384, make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]));
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      named_bar_arrive(7, kAll);
-    };
-    // values of tile j -> V, and the stage is free
-    auto write_v = [&](int j, float& vm) {
-      const uint32_t st = stage_of(j);
-      uint32_t wd[BV], hh[16];
-      tree_words<BV>(st + S::KC + t * (16 * BV) + w * (4 * BV), wd);
-      const uint32_t meta = lds32(st + S::KC + S::VC + 512 + t * 4);
-      tree_unpack<BV>(wd, hh);
-      // sigma = 2^e m with e >= -22 (so that 2^(e-2) t is exact in f16), 1 <= m < 2
-      // (or below for the smallest scales); 7 * 2^13 stays in range
-      const float sig = __half2float(__ushort_as_half(static_cast<unsigned short>(meta >> 16)));
-      const int e = max(static_cast<int>(__float_as_uint(sig) >> 23) - 127, -22);
-      vm = sig * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      const uint32_t s16 = __half_as_ushort(
-          __float2half_rn(__uint_as_float(static_cast<uint32_t>(125 + e) << 23)));
-      const uint32_t ss = s16 | (s16 << 16);
-      // byte g of z has coset bit g of this quarter in its top bit; a byte
-      // permute that repeats top bits makes the -2^(e-2) lanes of the set groups
-      const uint32_t z = ((meta >> (4 * w)) & 15u) * 0x10204080u;
-      const uint32_t neg = ss ^ 0x80008000u;
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int ga = tree_slot<BV>(2 * q) >> 3, gb = tree_slot<BV>(2 * q + 1) >> 3;
-        uint32_t m;  // (prmt's sign mode: __byte_perm has no form of it)
-        asm("prmt.b32 %0, %1, %1, %2;" : "=r"(m) : "r"(z), "r"(0x8888u | (ga * 0x11u) | (gb * 0x1100u)));
-        hh[q] = hfma2u(hh[q], ss, neg & m);
-      }
-      const uint32_t dst = base + S::V + (w >> 1) * 16384;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        sts128(dst + row_chunk(t, (w & 1) * 4 + c),
-               make_uint4(hh[4 * c], hh[4 * c + 1], hh[4 * c + 2], hh[4 * c + 3]));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + 8 * (j % kTreeStages));
-    };
-
-    float l[NR];
-#pragma unroll
-    for (int c = 0; c < NR; ++c) l[c] = 0.f;
-    bool started = false;  // some token of the split was valid (per warpgroup)
-    float4* fm = reinterpret_cast<float4*>(gen + S::FM) + w * (NR / 2);
-    int* wmax = reinterpret_cast<int*>(gen + S::WMax) + w * (NR * 4);
-
-    float kap, kap_next = 0.f, vm;
-    bool valid, valid_next = false;
-    uint4 cs[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) cs[x] = __ldg(ang + x * 128);
-    write_t(0, kap, valid);
-    write_k(cs, 0u);
-    write_v(0, vm);
-
-    for (int j = 0; j < nt; ++j) {
-      if (j + 1 < nt) {
-        write_t(j + 1, kap_next, valid_next);
-        ang += 16 * 128;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) cs[x] = __ldg(ang + x * 128);
-      }
-      // ---- softmax of tile j
-      tree_wait(bar_s, j & 1, dead);
-      tc_fence_after();
-      float y[NR];
-      constexpr int CH = NR < 16 ? NR : 16;
-#pragma unroll
-      for (int c0 = 0; c0 < NR; c0 += CH) {
-        uint32_t s[CH];
-        tmem_ld(tS + t_lane + w * NR + c0, s);
-        tmem_wait_ld(s);
+              for (int c = 0; c < 4; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
+              tmem_st(tO + t_lane + w * HN + h0 + c0, o);
+            }
+          }
+          tmem_wait_st();
+          named_bar_sync(bid, 128);  // the references are written, wmax is free
+        }
+        uint32_t pk[CH / 2];
 #pragma unroll
         for (int c = 0; c < CH; c += 2) {
-          const float4 f = fm[(c0 + c) / 2];
-          const float2 g = mul2(make_float2(f.x, f.y), make_float2(kap, kap));
-          const float2 v = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), g,
-                                make_float2(f.z, f.w));
-          y[c0 + c] = v.x;
-          y[c0 + c + 1] = v.y;
+          const float2 p = make_float2(ex2(y[c]), ex2(y[c + 1]));
+          const float2 s2 = add2(make_float2(l[h0 + c], l[h0 + c + 1]), p);
+          l[h0 + c] = s2.x;
+          l[h0 + c + 1] = s2.y;
+          const float2 pm = mul2(p, make_float2(vm, vm));
+          const __half2 ph = __floats2half2_rn(pm.x, pm.y);
+          pk[c / 2] = *reinterpret_cast<const uint32_t*>(&ph);
+        }
+        if (h0 == 0 && !raise) o_at_rest();
+#pragma unroll
+        for (int c = 0; c < CH; c += 8) {
+          const int col = w * HN + h0 + c;
+          sts128(base + S::P + (col / 64) * 16384 + row_chunk(t, (col % 64) >> 3),
+                 make_uint4(pk[c / 2], pk[c / 2 + 1], pk[c / 2 + 2], pk[c / 2 + 3]));
         }
       }
-      if (!valid) {
-#pragma unroll
-        for (int c = 0; c < NR; ++c) y[c] = -INFINITY;
-      }
-      float top = y[0];
-#pragma unroll
-      for (int c = 1; c < NR; ++c) top = fmaxf(top, y[c]);
-      if (named_bar_or(1 + w, 128, top > 14.0f || (!started && valid))) {
-        // exact column maxima of the tile, as ordered integers
-#pragma unroll
-        for (int c = 0; c < NR; ++c) {
-          const int i = __float_as_int(y[c]);
-          const int k = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
-          if (lane == 0) wmax[c * 4 + wl] = k;
-        }
-        named_bar_sync(1 + w, 128);
-        auto delta_of = [&](int c) {
-          const int4 k4 = *reinterpret_cast<const int4*>(wmax + c * 4);
-          const int k = max(max(k4.x, k4.y), max(k4.z, k4.w));
-          const float d = __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)) - 6.0f;
-          return started ? fmaxf(d, 0.f) : d;
-        };
-        if (t < NR) {
-          float* m = reinterpret_cast<float*>(fm + (t >> 1)) + 2 + (t & 1);
-          *m -= delta_of(t);
-        }
-#pragma unroll
-        for (int c0 = 0; c0 < NR; c0 += 4) {
-          float al[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float d = delta_of(c0 + c);
-            y[c0 + c] -= d;
-            al[c] = ex2(-d);
-            l[c0 + c] = started ? l[c0 + c] * al[c] : 0.f;
-          }
-          if (started && j > 0) {
-            uint32_t o[4];
-            tmem_ld(tO + t_lane + w * NR + c0, o);
-            tmem_wait_ld(o);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
-            tmem_st(tO + t_lane + w * NR + c0, o);
-          }
-        }
-        tmem_wait_st();
-        started = true;
-        named_bar_sync(1 + w, 128);  // the references are written, wmax is free
-      }
-      {
-        constexpr int kPB = NR >= 8 ? 8 : 4;  // rows per store
-        const uint32_t dst = base + S::P + (w * NR / 64) * 16384;
-#pragma unroll
-        for (int c0 = 0; c0 < NR; c0 += kPB) {
-          uint32_t pk[kPB / 2];
-#pragma unroll
-          for (int c = 0; c < kPB; c += 2) {
-            const float2 p = make_float2(ex2(y[c0 + c]), ex2(y[c0 + c + 1]));
-            const float2 s2 = add2(make_float2(l[c0 + c], l[c0 + c + 1]), p);
-            l[c0 + c] = s2.x;
-            l[c0 + c + 1] = s2.y;
-            const float2 pm = mul2(p, make_float2(vm, vm));
-            const __half2 ph = __floats2half2_rn(pm.x, pm.y);
-            pk[c / 2] = *reinterpret_cast<const uint32_t*>(&ph);
-          }
-          const int col = (w * NR + c0) % 64;
-          const uint32_t ad = dst + row_chunk(t, col >> 3) + (col & 7) * 2;
-          if constexpr (kPB == 8)
-            sts128(ad, make_uint4(pk[0], pk[1], pk[2], pk[3]));
-          else
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(ad), "r"(pk[0]), "r"(pk[1])
-                         : "memory");
-        }
-      }
+      started = started || raised;
       fence_proxy_async_smem();
       tc_fence_before();
-      named_bar_arrive(6, kAll);
-      if (j + 1 < nt) {
-        write_k(cs, (j + 1) & 1);
-        tree_wait(bar_o, j & 1, dead);  // V and P of tile j have been read
-        tc_fence_after();
-        write_v(j + 1, vm);
-      }
-      kap = kap_next;
-      valid = valid_next;
+      warp_arrive(bar_p, lane);
     }
-    tree_wait(bar_o, (nt - 1) & 1, dead);
+    tree_wait(bar_o(nt - 1), ((nt - 1) >> 1) & 1, dead);
     tc_fence_after();
 
     // ---- the split's sums: lane = code coordinate of this thread's TMEM lane
     const int coord = 32 * (t >> 5) + tree_slot<BV>(t & 31);
 #pragma unroll
-    for (int c0 = 0; c0 < NR; c0 += 4) {
-      uint32_t o[4];
-      tmem_ld(tO + t_lane + w * NR + c0, o);
+    for (int c0 = 0; c0 < HN; c0 += 8) {
+      uint32_t o[8];
+      tmem_ld(tO + t_lane + w * HN + c0, o);
       tmem_wait_ld(o);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int r = w * NR + c0 + c;
+      for (int c = 0; c < 8; ++c) {
+        const int r = w * HN + c0 + c;
         if (row0 + r < a.rows) part[r * part_row + 2 + coord] = __uint_as_float(o[c]);
       }
     }
     float* wsum = reinterpret_cast<float*>(wmax);
 #pragma unroll
-    for (int c = 0; c < NR; ++c) {
+    for (int c = 0; c < HN; ++c) {
       float s = l[c];
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (lane == 0) wsum[c * 4 + wl] = s;
     }
-    named_bar_sync(1 + w, 128);
-    if (t < NR && row0 + w * NR + t < a.rows) {
+    named_bar_sync(bid, 128);
+    if (t < HN && row0 + w * HN + t < a.rows) {
       const float4 s = *reinterpret_cast<const float4*>(wsum + t * 4);
       const float* m = reinterpret_cast<const float*>(fm + (t >> 1)) + 2 + (t & 1);
-      float* p = part + (w * NR + t) * part_row;
+      float* p = part + (w * HN + t) * part_row;
       p[0] = started ? -*m : -INFINITY;
       p[1] = (s.x + s.y) + (s.z + s.w);
     }
     tc_fence_before();
+  } else {
+    // ---------------------------------------------------------- the MMAs
+    regs_dec<TreeRegs<N>::Issue>();
+    // low words of the matrix descriptors (address >> 4, leading offset above
+    // bit 16), so that an instruction costs one addition per operand
+    const uint32_t b4 = base >> 4;
+    constexpr uint32_t iX = idesc_f16_f32(128, 64), iC = idesc_f16_f32(128, 128);
+    constexpr uint32_t iS = idesc_f16_f32(128, N), iO = idesc_f16_f32(128, N) | kIdescAMn | kIdescBMn;
+    const uint32_t one = elect_lane();
+    // two tiles per round, so that everything that an instruction names by
+    // the tile's parity is a constant
+    if (warp == 20) {  // X = t H
+      auto step = [&](int j, auto parity) {
+        constexpr uint32_t d = kTmX + decltype(parity)::value * 128;
+        tree_wait(bar_t, j & 1, dead);
+        tc_fence_after();
+        umma_f16_if(one, d, desc_plain(base + S::CA, 2048, 128), desc_plain(base + S::CB, 2048, 128),
+                    iC, 0u);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_f16_if(one, d + 64 * hf, tree_desc(b4 + ((S::T + hf * 16384 + k * 32) >> 4), 1u),
+                        tree_desc(b4 + ((S::H + k * 32) >> 4), 1u), iX, 1u);
+        umma_commit_if(one, bar_x);
+      };
+      for (int j = 0; j < nt; j += 2) {
+        step(j, Parity<0>());
+        if (j + 1 < nt) step(j + 1, Parity<1>());
+      }
+    } else if (warp == 21) {  // S = keys Q^T
+      auto step = [&](int j, auto parity) {
+        constexpr int q = decltype(parity)::value;
+        tree_wait(bar_k(q), (j >> 1) & 1, dead);
+        if (j > 0) tree_wait(bar_sf, (j - 1) & 1, dead);
+        tc_fence_after();
+        constexpr uint32_t kb = S::K + (q % S::KBufs) * 32768;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          umma_f16_if(one, kTmS, tree_desc(b4 + ((kb + (k >> 2) * 16384 + (k & 3) * 32) >> 4), 1u),
+                      tree_desc(b4 + ((S::Q + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), 1u), iS,
+                      k > 0);
+        umma_commit_if(one, bar_s(q));
+        // orders the key scales, which this warp's wait for the keys has
+        // acquired, before the softmax threads' reads
+        if (lane == 0) mbar_arrive(bar_s(q));
+        __syncwarp();
+      };
+      for (int j = 0; j < nt; j += 2) {
+        step(j, Parity<0>());
+        if (j + 1 < nt) step(j + 1, Parity<1>());
+      }
+    } else if (warp == 22) {  // O += V P
+      auto step = [&](int j, auto parity) {
+        constexpr int q = decltype(parity)::value;
+        tree_wait(bar_v(q), (j >> 1) & 1, dead);
+        tree_wait(bar_p, j & 1, dead);
+        tc_fence_after();
+        const uint32_t more = j > 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          umma_f16_if(one, kTmS + N, tree_desc(b4 + ((S::V + q * 32768 + k * 2048) >> 4), 16384u >> 4),
+                      tree_desc(b4 + ((S::P + k * 2048) >> 4), 16384u >> 4), iO, k > 0 ? 1u : more);
+        umma_commit_if(one, bar_o(q));
+      };
+      for (int j = 0; j < nt; j += 2) {
+        step(j, Parity<0>());
+        if (j + 1 < nt) step(j + 1, Parity<1>());
+      }
+    }
   }
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 20) {
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
   }
@@ -851,7 +972,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a) {
 
 // ------------------------------------------------------------------ launch
 struct TreePlan {
-  int nr, rblocks;
+  int cols, rblocks;
   int64_t tiles, per, nsplit;
 };
 
@@ -863,8 +984,8 @@ static TreePlan tree_plan(int units, int heads, int G, int nodes, int64_t n) {
   const int64_t rows = static_cast<int64_t>(nodes) * G;
   p.rblocks = static_cast<int>((rows + 127) / 128);
   const int64_t cols = (rows + p.rblocks - 1) / p.rblocks;
-  p.nr = cols <= 16 ? 4 : (cols <= 32 ? 8 : (cols <= 64 ? 16 : 32));
-  p.rblocks = static_cast<int>((rows + 4 * p.nr - 1) / (4 * p.nr));
+  p.cols = cols <= 16 ? 16 : (cols <= 32 ? 32 : (cols <= 64 ? 64 : 128));
+  p.rblocks = static_cast<int>((rows + p.cols - 1) / p.cols);
   p.tiles = (n + kTreeTile - 1) / kTreeTile;
   if (p.tiles < 1) p.tiles = 1;
   const int64_t ctas = static_cast<int64_t>(units) * heads * p.rblocks;
@@ -900,24 +1021,23 @@ int64_t tree_ctas(int units, int heads, int G, int nodes, int64_t n) {
   return a > b ? a : b;
 }
 
-template <int BK, int BV, int NR>
-static cudaError_t launch_tree_nr(const TreeArgs& a, int64_t grid, cudaStream_t stream) {
-  constexpr int smem = TreeSmem<BK, BV, NR>::Bytes;
-  cudaError_t err = cudaFuncSetAttribute(tree_partial_kernel<BK, BV, NR>,
+template <int BK, int BV, int N>
+static cudaError_t launch_tree_n(const TreeArgs& a, int64_t grid, cudaStream_t stream) {
+  constexpr int smem = TreeSmem<BK, BV, N>::Bytes;
+  cudaError_t err = cudaFuncSetAttribute(tree_partial_kernel<BK, BV, N>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  tree_partial_kernel<BK, BV, NR>
-      <<<static_cast<unsigned>(grid), kTreeThreads, smem, stream>>>(a);
+  tree_partial_kernel<BK, BV, N><<<static_cast<unsigned>(grid), kTreeThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
 template <int BK, int BV>
-static cudaError_t launch_tree_partial(const TreeArgs& a, int nr, int64_t grid, cudaStream_t stream) {
-  switch (nr) {
-    case 4: return launch_tree_nr<BK, BV, 4>(a, grid, stream);
-    case 8: return launch_tree_nr<BK, BV, 8>(a, grid, stream);
-    case 16: return launch_tree_nr<BK, BV, 16>(a, grid, stream);
-    default: return launch_tree_nr<BK, BV, 32>(a, grid, stream);
+static cudaError_t launch_tree_partial(const TreeArgs& a, int64_t grid, cudaStream_t stream) {
+  switch (a.ncols) {
+    case 16: return launch_tree_n<BK, BV, 16>(a, grid, stream);
+    case 32: return launch_tree_n<BK, BV, 32>(a, grid, stream);
+    case 64: return launch_tree_n<BK, BV, 64>(a, grid, stream);
+    default: return launch_tree_n<BK, BV, 128>(a, grid, stream);
   }
 }
 
@@ -928,7 +1048,8 @@ cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream) {
   a.n_a = (L.rope_max_pos + 255) / 256;
   if (L.n > 0) {
     const TreePlan p = tree_plan(L.units, L.heads, L.G, L.nodes, L.n);
-    a.ncols = 4 * p.nr;
+    a.ncols = p.cols;
+    a.page = make_fastdiv(static_cast<uint32_t>(L.table ? L.page_size : 1));
     a.rblocks = p.rblocks;
     a.tiles = p.tiles;
     a.per = p.per;
@@ -943,10 +1064,10 @@ cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream) {
     if (err != cudaSuccess) return err;
     const int64_t grid = static_cast<int64_t>(L.units) * L.heads * p.rblocks * p.nsplit;
     const int bk = L.k_in.bits, bv = L.v_in.bits;
-    err = bk == 3 ? (bv == 3 ? launch_tree_partial<3, 3>(a, p.nr, grid, stream)
-                             : launch_tree_partial<3, 2>(a, p.nr, grid, stream))
-                  : (bv == 3 ? launch_tree_partial<2, 3>(a, p.nr, grid, stream)
-                             : launch_tree_partial<2, 2>(a, p.nr, grid, stream));
+    err = bk == 3 ? (bv == 3 ? launch_tree_partial<3, 3>(a, grid, stream)
+                             : launch_tree_partial<3, 2>(a, grid, stream))
+                  : (bv == 3 ? launch_tree_partial<2, 3>(a, grid, stream)
+                             : launch_tree_partial<2, 2>(a, grid, stream));
     if (err != cudaSuccess) return err;
   }
   const int64_t rows = static_cast<int64_t>(L.units) * L.heads * a.rows;

@@ -6,12 +6,16 @@ Tree attention, per output element with the exact softmax weights p_t and
 scores s_t of the row (fp64):
   |out - ref| <= 2^-8 |ref| + B sum_t p_t |v_t|,   B = 2 ds + 2^-10 + 2^-16,
   |lse - ref| <= ds + 2^-18 (1 + |lse|),
-with ds the largest score error: a key coordinate is rounded to f16 (2^-11)
-after a rotation whose cos and sin are rounded to f16 (2^-11 each of values up
-to sqrt 2, both multiplied by coordinates of the same pair), so
-  ds = scale max_t sum_i (|q_i| + |q_i'|) |k_ti| 2^-11 * 2.5
-over RoPE partners i, i' (the fp32 sums add below 2^-20 of the same sum); the
-weights and the scaled codes are rounded to f16 (2^-11 each), a weight error
+with ds the largest score error.  A rotated key pair of length r (r <= |k_i| +
+|k_i'| over RoPE partners i, i') is formed in f16 as u c' + v s', u = (x_i +
+x_i')/2 and v = (x_i - x_i')/2 exact, c' = cos - sin, s' = cos + sin: |u| + |v| =
+max(|x_i|, |x_i'|) <= r, |v| <= r / sqrt 2 and |u| likewise.  c' and s' are below
+sqrt 2, rounded by at most 2^-11 (together 2^-11 r), the product v s' by 2^-11
+of at most r, the sum by 2^-11 |k_i|: at most 2^-11 (2 r + |k_i|), so
+  ds = scale max_t sum_i (|q_i| + |q_i'|) |k_ti| 2^-11 * 3
+(sum_i |q_i| r <= sum_i (|q_i| + |q_i'|) |k_ti| pair by pair, and |q_i| |k_ti|
+is part of it; the fp32 sums add below 2^-20 of the same sum: 2^-18); the
+weights are rounded to f16 (2^-11; the scaled codes are exact), a weight error
 e^ds acts on numerator and sum (2 ds), fp32 sums add below 2^-16, and the
 output is rounded to bf16 (half a step: 2^-8 relative).
 """
@@ -379,7 +383,7 @@ def ref_tree(q, Kn, Vn, ks, vs, lens, table, P, positions, pos_base, theta, mask
             with np.errstate(divide="ignore"):
                 lse[u, j] = (np.where(np.isinf(m), 0, m) + np.log(l))[:, 0]
             qq = np.abs(q[u, j]) + np.abs(np.roll(q[u, j], 64, -1))
-            ds = abs(scale) * (qq @ np.abs(k[h]).T).max(-1) * 2.5 * 2.0 ** -11 if n else np.zeros(M)
+            ds = abs(scale) * (qq @ np.abs(k[h]).T).max(-1) * 3 * 2.0 ** -11 if n else np.zeros(M)
             ds = ds + 2.0 ** -18
             ob[u, j] = 2.0 ** -8 * np.abs(out[u, j]) + \
                 (2 * ds + (2.0 ** -10 if n else 0) + 2.0 ** -16)[:, None] * (pr @ np.abs(va))

@@ -28,12 +28,13 @@
 // maxima; the others only compare (one vote per tile and warpgroup).
 //
 // One CTA per SM, its warpgroups specialised so that the phases of different
-// tiles overlap: two warpgroups make keys (a token per thread and half of its
-// coordinates: codes -> t, then X -> rotated keys), one makes values, two do
-// the softmax (half of the query rows each), and the last one's warps issue
-// the three products.  X is double buffered in TMEM, so the codes of tile j+1
-// go to the tensor cores before tile j is rotated.  Registers are moved to
-// the softmax warpgroups, which hold a sum per query row.  The work of a
+// tiles overlap: two or four warpgroups make keys (a token per thread and a
+// part of its coordinates: codes -> t, then X -> rotated keys), one makes
+// values, two do the softmax (half of the query rows each), and the last
+// one's warps issue the three products.  X is double buffered in TMEM, so the
+// codes of tile j+1 go to the tensor cores before tile j is rotated.
+// Registers are moved to the softmax warpgroups, which hold a sum per query
+// row.  The work of a
 // launch is split over the tokens (flash decoding) to fill the 148 SMs;
 // tree_combine_kernel merges the splits, applies H and attends the draft
 // nodes in fp32.
@@ -49,10 +50,10 @@ namespace nq {
 
 constexpr int kTreeTile = 128;     // tokens per tile
 constexpr int kTreePart = 2 + kD;  // a split's m (log2 units), l, sums[128] in the code domain
-constexpr int kTreeThreads = 768;  // keys 2 x 128, values 128, softmax 2 x 128, issue 128
+constexpr float kTreeStart = 4.0f, kTreeTop = 14.0f;  // log2 of a column's largest weight: see below
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr uint32_t kTreeWaitLimit = 1u << 20;
+constexpr uint32_t kTreeWaitLimit = 1u << 16, kTreeWaitNs = 16384;  // about a second
 constexpr uint32_t kErrTreeTimeout = 4u;
 
 struct TreeArgs {
@@ -151,10 +152,27 @@ __host__ __device__ constexpr uint32_t f16_bits(float v) {
 }
 __host__ __device__ constexpr uint32_t f16_pair(float lo, float hi) { return f16_bits(lo) | (f16_bits(hi) << 16); }
 
+__device__ __forceinline__ uint32_t hadd2u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
+}
+
+// The f16 pairs of coset bits that a 32-code run needs: byte g of z has the
+// coset bit of group g in its top bit; a byte permute that repeats top bits
+// makes the lanes' masks.
+__device__ __forceinline__ uint32_t coset_bytes(uint32_t bits4) { return (bits4 & 15u) * 0x10204080u; }
+__device__ __forceinline__ uint32_t coset_mask(uint32_t z, int ga, int gb) {
+  uint32_t m;  // (prmt's sign mode: __byte_perm has no form of it)
+  asm("prmt.b32 %0, %1, %1, %2;"
+      : "=r"(m)
+      : "r"(z), "r"(0x8888u | (ga * 0x11u) | (gb * 0x1100u)));
+  return m;
 }
 
 // The pair with fields at bits dl (low lane) and 16 + dh of v -> 2j - (2^b - 2).
@@ -203,9 +221,8 @@ __device__ __forceinline__ void tree_unpack(const uint32_t (&w)[BITS], uint32_t 
   }
 }
 
-// Row t, 16-byte chunk c of an operand of 128-byte swizzled rows (the K-major
-// layout with a token per row and the MN-major one with a token per k are the
-// same addresses).
+// Row t, 16-byte chunk c of an operand of 128-byte swizzled rows (K-major: an
+// output row per row; MN-major: a token, the k index, per row).
 __device__ __forceinline__ uint32_t row_chunk(int t, int c) {
   return static_cast<uint32_t>((t >> 3) * 1024 + (t & 7) * 128 + ((c ^ (t & 7)) << 4));
 }
@@ -219,33 +236,37 @@ __device__ __forceinline__ float ex2(float x) {
 // ------------------------------------------------------------ shared memory
 template <int BK, int BV, int N>
 struct TreeSmem {
-  static constexpr int KBufs = N > 64 ? 1 : 2;          // what fits
-  static constexpr int T = 0;                           // t of the keys: 2 x (128 rows x 128 B)
-  static constexpr int K = T + 32768;                   // rotated keys, the same
-  static constexpr int V = K + KBufs * 32768;           // scaled value codes, two tiles
-  static constexpr int P = V + 2 * 32768;               // weights: N/64 blocks of 128 rows
-  static constexpr int Q = P + (N > 64 ? 2 : 1) * 16384;  // queries: 2 x (N rows x 128 B)
+  static constexpr int V = 0;                           // scaled value codes, two tiles of
+                                                        // 2 x (128 rows x 128 B)
+  static constexpr int PBytes = (N > 64 ? 2 : 1) * 16384;  // weights: N/64 blocks of 128 rows
+  static constexpr int P = V + 2 * 32768;               // of two tiles
+  static constexpr int Q = P + 2 * PBytes;              // queries: 2 x (N rows x 128 B)
   static constexpr int H = Q + N * 256;                 // H64, 64 rows x 128 B
-  static constexpr int CA = H + 8192;                   // coset bits of the tile, 128 x 16 f16
-  static constexpr int CB = CA + 4096;                  // their rows of H, 128 x 16 f16
-  static constexpr int Kap = CB + 4096;                 // key scales of 8 tiles (-1: no token)
+  static constexpr int Kap = H + 8192;                  // key scales of 8 tiles (-1: no token)
   static constexpr int Vm = Kap + 8 * 512;              // value scale mantissas of 8 tiles
   static constexpr int FM = Vm + 8 * 512;               // (f0, f1, -m0, -m1) per row pair
   static constexpr int WMax = FM + N * 8;               // [N][4 warps]
-  static constexpr int Bars = WMax + N * 16;
+  static constexpr int WOr = WMax + N * 16;             // [2][4 warps]
+  static constexpr int Bars = WOr + 32;
   static constexpr int Bytes = Bars + 128 + 1024;       // 1 KB of slack to align the base
   static_assert(Bytes <= 232448, "one CTA per SM within 227 KB");
+  // TMEM columns (all 512 are allocated): X (one or two tiles), S, O, and the
+  // A operands T and K (two f16 per column)
+  static constexpr int XBufs = N > 64 ? 1 : 2, KBufs = N > 32 ? 1 : 2;
+  static constexpr uint32_t tX = 0, tS = XBufs * 128, tO = tS + N, tT = tO + N, tK = tT + 64;
+  static_assert(tK + KBufs * 64 <= 512, "tensor memory");
 };
 
 // Bounded wait; past the limit the error word is set and `dead` makes every
 // later wait of the CTA return at once (its results are then unspecified).
-// A wait names its phase by parity, so no phase may complete twice before a
-// waiter has looked: each barrier's next phase needs something that its
-// waiters do after their wait for this one.
+// A wait names its phase by parity, so a barrier must neither be a phase
+// further than the one waited for nor a phase behind: each barrier's next
+// phase needs something that its waiters do after their wait for this one,
+// and every waiter takes the phases in order.
 __device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
-  bool done = mbar_try_wait(bar, parity);
-  for (uint32_t spin = 0; !done && spin < kTreeWaitLimit; ++spin)
-    done = mbar_try_wait(bar, parity) || *dead;
+  bool done = mbar_try_wait_for(bar, parity, kTreeWaitNs);
+  for (uint32_t spin = 1; !done && spin < kTreeWaitLimit; ++spin)
+    done = mbar_try_wait_for(bar, parity, kTreeWaitNs) || *dead;
   if (!done) {
     *dead = 1u;
     atomicOr(&g_nq_error, kErrTreeTimeout);
@@ -275,14 +296,26 @@ template <int REGS>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
-// Registers per thread of the roles, out of the 768 x 80 = 61440 that the block
-// is launched with.
+// Warpgroups of the roles (KW: threads that share a token's key) and their
+// registers per thread, out of Launch x threads that the block starts with.
+// Up to 64 columns the key warpgroups bound the pipeline, so they are four;
+// with 128 the softmax does, and it needs the registers.
 template <int N>
-struct TreeRegs {
-  static constexpr int Softmax = N > 64 ? 128 : 96, Keys = N > 64 ? 64 : 80,
-                       Values = N > 64 ? 56 : 80, Issue = 40;
-  static_assert(2 * Softmax + 2 * Keys + Values + Issue <= 6 * 80, "the launch's registers");
+struct TreeRoles {
+  static constexpr int KW = N > 64 ? 2 : 4;
+  static constexpr int Values0 = 4 * KW, Softmax0 = Values0 + 4, Issue0 = Softmax0 + 8;  // warps
+  static constexpr int Threads = 32 * (Issue0 + 4);
+  static constexpr int Launch = N > 64 ? 80 : 64;
+  static constexpr int Softmax = N > 64 ? 128 : (N > 32 ? 96 : 64), Keys = N > 64 ? 64 : (N > 32 ? 56 : 64),
+                       Values = N > 64 ? 56 : (N > 32 ? 56 : 64), Issue = N > 64 ? 40 : (N > 32 ? 32 : 64);
+  static_assert(2 * Softmax + KW * Keys + Values + Issue <= Threads / 128 * Launch,
+                "the launch's registers");
 };
+template <int LAUNCH, int WANT>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (WANT > LAUNCH) regs_inc<WANT>();
+  if constexpr (WANT < LAUNCH) regs_dec<WANT>();
+}
 
 // The tokens of one thread, tile by tile: the unit or page that holds the
 // token (-1: no token) and its slot there.  The page entry of the next tile is
@@ -320,20 +353,16 @@ __device__ __forceinline__ void value_scale(uint32_t meta, float& m, int& e) {
   m = sig * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
-constexpr uint32_t kTmX = 0, kTmS = 256;  // TMEM columns: X twice, S, O
-
 template <int V>
 struct Parity {
   static constexpr int value = V;
 };
 
 template <int BK, int BV, int N>
-__global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(const TreeArgs a) {
   using S = TreeSmem<BK, BV, N>;
+  using R = TreeRoles<N>;
+  constexpr int KW = R::KW;
   extern __shared__ __align__(1024) unsigned char tree_smem[];
   const uint32_t raw = smem_u32(tree_smem);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -344,13 +373,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
   // written, weights written, O done (the scales of a tile are written with
   // its codes).  Where a buffer is double, so is its barrier: tile j uses
   // barrier j & 1 in its phase j >> 1.
-  const uint32_t bar_t = base + S::Bars, bar_x = bar_t + 8, bar_sf = bar_t + 16, bar_p = bar_t + 24;
+  const uint32_t bar_t = base + S::Bars, bar_x = bar_t + 8, bar_sf = bar_t + 16;
+  const uint32_t bar_xf = bar_t + 24;  // X read (where it is single)
   auto bar_k = [&](int j) { return bar_t + 32 + 8 * (j & 1); };
   auto bar_s = [&](int j) { return bar_t + 48 + 8 * (j & 1); };
   auto bar_v = [&](int j) { return bar_t + 64 + 8 * (j & 1); };
   auto bar_o = [&](int j) { return bar_t + 80 + 8 * (j & 1); };
-  const uint32_t tslot = bar_t + 96;
-  volatile uint32_t* dead = reinterpret_cast<volatile uint32_t*>(gen + S::Bars + 100);
+  auto bar_p = [&](int j) { return bar_t + 96 + 8 * (j & 1); };
+  const uint32_t tslot = bar_t + 112;
+  volatile uint32_t* dead = reinterpret_cast<volatile uint32_t*>(gen + S::Bars + 116);
 
   // block index -> (split, unit * heads + head, row block): the row blocks and
   // heads of the same tokens are neighbours (their codes and angles meet in L2)
@@ -376,20 +407,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
   }
 
   // ---- setup: barriers, TMEM, constant operands, queries
-  constexpr uint32_t kCols = 512;  // X twice, S, O
-  if (warp == 20) {
+  constexpr uint32_t kCols = 512;
+  if (warp == R::Issue0) {
     tmem_alloc(tslot, kCols);
     tmem_relinquish();
   }
   if (tid == 0) {
-    mbar_init(bar_t, 8);
+    mbar_init(bar_t, 4 * KW);
     mbar_init(bar_x, 1);
+    mbar_init(bar_xf, 4 * KW);
     mbar_init(bar_sf, 8);
-    mbar_init(bar_p, 8);
     for (int j = 0; j < 2; ++j) {
-      mbar_init(bar_k(j), 8);
+      mbar_init(bar_k(j), 4 * KW);
       mbar_init(bar_s(j), 2);  // the products, and their issuer (see there)
       mbar_init(bar_v(j), 4);
+      mbar_init(bar_p(j), 8);
       mbar_init(bar_o(j), 1);
     }
     *dead = 0u;
@@ -410,19 +442,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
       v[i] = pr;
     }
     sts128(base + S::H + row_chunk(n, c), make_uint4(v[0], v[1], v[2], v[3]));
-  } else {  // coset slots: output row n, groups 8c .. 8c+7 (u rows: c = 0, v rows: c = 1)
-    const int n = (tid - 512) >> 1, c = tid & 1;
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-    if ((n >> 6) == c && (n & 7) == 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t s0 = __popc(n & 63 & (8 * (2 * i))) & 1, s1 = __popc(n & 63 & (8 * (2 * i + 1))) & 1;
-        v[i] = (s0 ? 0x4800u : 0xC800u) | ((s1 ? 0x4800u : 0xC800u) << 16);  // -8 (-1)^popc
-      }
-    }
-    sts128(base + S::CB + c * 2048 + n * 16, make_uint4(v[0], v[1], v[2], v[3]));
   }
-  for (int r = warp; r < N; r += kTreeThreads / 32) {
+  for (int r = warp; r < N; r += R::Threads / 32) {
     const int row = row0 + r;
     float q[4] = {0.f, 0.f, 0.f, 0.f};
     if (row < a.rows) {
@@ -462,89 +483,93 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
   __syncthreads();
   tc_fence_after();
   // the whole of TMEM is allocated (512 columns), so it starts at column 0
-  const uint32_t tmem = 0u, tX = kTmX, tS = kTmS, tO = kTmS + N;
+  constexpr uint32_t tS = S::tS, tO = S::tO;
   const int t = tid & 127;
   const uint32_t t_lane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
 
-  if (warp < 8) {
+  if (warp < R::Values0) {
     // ------------------------------------------------------------- keys
-    // Thread (t, kw): token t, codes 64 kw .. +63, frequencies 32 kw .. +31.
-    if constexpr (TreeRegs<N>::Keys < 80) regs_dec<TreeRegs<N>::Keys>();
+    // Thread (t, kw): token t, 128 / KW codes and 64 / KW frequencies.
+    set_regs<R::Launch, R::Keys>();
+    constexpr int NU = 4 / KW;           // runs of 32 codes
+    constexpr int NQ = 8 / KW;           // runs of 8 frequencies
     const int kw = warp >> 2;
-    const uint4* ang = a.angles + u * a.angle_stride + ((split * a.per * 4 + 2 * kw) * 4) * 128 + t;
+    const uint4* ang = a.angles + u * a.angle_stride + ((split * a.per * 4) * 4 + 2 * NQ * kw) * 128 + t;
     TokenWalk walk(a, u, t0 + t, t1);
-    uint32_t wd[2 * BK], meta, vmeta = 0u;
+    // a quarter of a 3-bit vector is three words out of one or two 16-byte
+    // chunks: these are loaded whole (one strided access instead of three) and
+    // picked from when they are used, so that nothing waits for the loads
+    constexpr bool kChunks = NU * BK == 3;
+    uint32_t wd[kChunks ? 8 : NU * BK], meta, vmeta;
     int32_t lead;  // where the token of the tile after the loaded one is
     uint32_t slot;
     const int64_t khead = h * L.k_in.head_stride, vhead = h * L.v_in.head_stride;
+    // Loads whatever the token: without one, vector 0, whose bits are not used
+    // (a branch here makes the compiler move the loaded values at its end,
+    // which waits for them).
+    bool held;  // the loaded tile's token exists
     auto load = [&]() {
-      if (lead >= 0) {
-        const int64_t v = lead * L.k_in.unit_stride + khead + slot;
-        const uint32_t* src = L.k_in.codes + v * (4 * BK) + kw * (2 * BK);
-        if constexpr (BK == 2) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
-          wd[0] = x.x, wd[1] = x.y, wd[2] = x.z, wd[3] = x.w;
-        } else {
+      held = lead >= 0;
+      const int64_t v = held ? lead * L.k_in.unit_stride + khead + slot : 0;
+      const uint32_t* src = L.k_in.codes + v * (4 * BK) + (kChunks ? (3 * kw) / 4 * 4 : kw * (NU * BK));
+      if constexpr (NU * BK == 4 || kChunks) {
 #pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(src) + i);
-            wd[2 * i] = x.x, wd[2 * i + 1] = x.y;
-          }
+        for (int i = 0; i < (kChunks ? 2 : 1); ++i) {
+          // (the second chunk of an outer quarter is not used: the first again)
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + (kw == 1 || kw == 2 ? i : 0));
+          wd[4 * i] = x.x, wd[4 * i + 1] = x.y, wd[4 * i + 2] = x.z, wd[4 * i + 3] = x.w;
         }
-        meta = __ldg(L.k_in.meta + v);
-        if (kw == 1) vmeta = __ldg(L.v_in.meta + (lead * L.v_in.unit_stride + vhead + slot));
-      } else {  // a NaN scale marks it: the codec's scales are finite
+      } else {
 #pragma unroll
-        for (int i = 0; i < 2 * BK; ++i) wd[i] = 0u;
-        meta = 0xFFFF0000u;
+        for (int i = 0; i < NU * BK / 2; ++i) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(src) + i);
+          wd[2 * i] = x.x, wd[2 * i + 1] = x.y;
+        }
       }
+      meta = __ldg(L.k_in.meta + v);
+      vmeta = __ldg(L.v_in.meta + (held ? lead * L.v_in.unit_stride + vhead + slot : 0));
     };
-    // codes of tile j -> T and coset slots; then the loads of tile j+1
+    // codes of tile j -> T; then the loads of tile j+1
     auto write_t = [&](int j) {
-      const uint32_t dst = base + S::T + kw * 16384;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < NU; ++s) {
+        const int run = NU * kw + s;  // codes 32 run .. 32 run + 31
         uint32_t w[BK], hh[16];
 #pragma unroll
-        for (int i = 0; i < BK; ++i) w[i] = wd[s * BK + i];
+        for (int i = 0; i < BK; ++i)
+          w[i] = !kChunks ? wd[s * BK + i]
+                          : (kw == 0 ? wd[i] : (kw == 1 ? wd[i + 3] : (kw == 2 ? wd[i + 2] : wd[i + 1])));
         tree_unpack<BK>(w, hh);
+        const uint32_t z = coset_bytes(meta >> (4 * run));
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          sts128(dst + row_chunk(t, 4 * s + c),
-                 make_uint4(hh[4 * c], hh[4 * c + 1], hh[4 * c + 2], hh[4 * c + 3]));
+        for (int q = 0; q < 16; ++q)  // - h (-1.0 = 0xBC00), exact
+          hh[q] = hadd2u(hh[q], 0xBC00BC00u & coset_mask(z, tree_slot<BK>(2 * q) >> 3,
+                                                         tree_slot<BK>(2 * q + 1) >> 3));
+        tmem_st(S::tT + t_lane + 16 * run, hh);
       }
-      // coset bits 8kw .. 8kw+7 as f16 0 or 1 (bit 2u at bit 0 of y >> 2u, bit
-      // 2u+1 at bit 16)
-      const uint32_t cb = (meta >> (8 * kw)) & 255u, y = cb | (cb << 15);
-      sts128(base + S::CA + kw * 2048 + t * 16,
-             make_uint4((y & 0x10001u) * 0x3C00u, ((y >> 2) & 0x10001u) * 0x3C00u,
-                        ((y >> 4) & 0x10001u) * 0x3C00u, ((y >> 6) & 0x10001u) * 0x3C00u));
-      if (kw == 0) {
+      if (kw == KW - 2) {
         const float sig = __half2float(__ushort_as_half(static_cast<unsigned short>(meta >> 16)));
         const float kap = __fmul_rn(__fmul_rn(sig, 0.5f), __uint_as_float(kCBits));
-        reinterpret_cast<float*>(gen + S::Kap)[(j & 7) * 128 + t] = kap >= 0.f ? kap : -1.0f;
-      } else {
+        reinterpret_cast<float*>(gen + S::Kap)[(j & 7) * 128 + t] = held ? kap : -1.0f;
+      }
+      if (kw == KW - 1) {
         float m;
         int e;
-        value_scale(vmeta, m, e);
+        value_scale(held ? vmeta : 0u, m, e);
         reinterpret_cast<float*>(gen + S::Vm)[(j & 7) * 128 + t] = m;
       }
-      fence_proxy_async_smem();
+      tmem_wait_st();
       tc_fence_before();
       warp_arrive(bar_t, lane);
       load();
       walk.next(lead, slot);
-      if (lead >= 0) {
-        const int64_t v = lead * L.k_in.unit_stride + khead + slot;
-        prefetch_l2(L.k_in.codes + v * (4 * BK) + kw * (2 * BK));
-        if (kw == 0) prefetch_l2(L.k_in.meta + v);
-      }
     };
     walk.next(lead, slot);
     load();
     walk.next(lead, slot);
     write_t(0);
     for (int j = 0; j < nt; ++j) {
+      // the angles of two runs of frequencies, those of the next two follow
       uint4 cs[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) cs[x] = __ldg(ang + x * 128);
@@ -553,15 +578,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
       if (j + 1 < nt) write_t(j + 1);
       // the keys that this buffer held have been read
       if (j >= S::KBufs) tree_wait(bar_s(j - S::KBufs), ((j - S::KBufs) >> 1) & 1, dead);
-      const uint32_t kb = base + S::K + (j % S::KBufs) * 32768;
-      const uint32_t x0 = tX + t_lane + (j & 1) * 128 + 32 * kw;
+      tc_fence_after();
+      const uint32_t kb = S::tK + t_lane + (j % S::KBufs) * 64 + 4 * NQ * kw;
+      const uint32_t x0 = S::tX + t_lane + (j % S::XBufs) * 128 + 8 * NQ * kw;
+      uint32_t uu[2][8], vv[2][8];
+      tmem_ld(x0, uu[0]);
+      tmem_ld(x0 + 64, vv[0]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // eight frequencies at a time
-        uint32_t uu[8], vv[8];
-        tmem_ld(x0 + 8 * q, uu);
-        tmem_ld(x0 + 64 + 8 * q, vv);
-        tmem_wait_ld(uu);
-        tmem_wait_ld(vv);
+      for (int q = 0; q < NQ; ++q) {  // eight frequencies at a time
+        tmem_wait_ld(uu[q & 1]);
+        tmem_wait_ld(vv[q & 1]);
+        if (q + 1 < NQ) {
+          tmem_ld(x0 + 8 * (q + 1), uu[(q + 1) & 1]);
+          tmem_ld(x0 + 64 + 8 * (q + 1), vv[(q + 1) & 1]);
+        } else if (S::XBufs == 1) {  // X has been read
+          tc_fence_before();
+          warp_arrive(bar_xf, lane);
+        }
         uint32_t lo[4], hi[4];
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
@@ -570,43 +603,45 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
           const __half2 c = *reinterpret_cast<const __half2*>(&cw);
           const __half2 s = *reinterpret_cast<const __half2*>(&sw);
           // u and v are integers up to 448: exact in f16
-          const __half2 U = __floats2half2_rn(__uint_as_float(uu[2 * f]), __uint_as_float(uu[2 * f + 1]));
-          const __half2 V = __floats2half2_rn(__uint_as_float(vv[2 * f]), __uint_as_float(vv[2 * f + 1]));
+          const __half2 U = __floats2half2_rn(__uint_as_float(uu[q & 1][2 * f]),
+                                              __uint_as_float(uu[q & 1][2 * f + 1]));
+          const __half2 V = __floats2half2_rn(__uint_as_float(vv[q & 1][2 * f]),
+                                              __uint_as_float(vv[q & 1][2 * f + 1]));
           const __half2 a0 = __hfma2(U, c, __hmul2(V, s));
           const __half2 a1 = __hfma2(__hneg2(V), c, __hmul2(U, s));
           lo[f] = *reinterpret_cast<const uint32_t*>(&a0);
           hi[f] = *reinterpret_cast<const uint32_t*>(&a1);
         }
-        if (q < 2) {  // the angles of the frequencies after the next eight
+        if (q + 2 < NQ) {
           cs[2 * q] = __ldg(ang + (4 + 2 * q) * 128);
           cs[2 * q + 1] = __ldg(ang + (5 + 2 * q) * 128);
         }
-        const uint32_t dst = kb + row_chunk(t, 4 * kw + q);
-        sts128(dst, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        sts128(dst + 16384, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        tmem_st(kb + 4 * q, lo);
+        tmem_st(kb + 32 + 4 * q, hi);
       }
       ang += 16 * 128;
-      fence_proxy_async_smem();
+      tmem_wait_st();
       tc_fence_before();
       warp_arrive(bar_k(j), lane);
     }
-  } else if (warp < 12) {
+  } else if (warp < R::Softmax0) {
     // ------------------------------------------------------------ values
-    if constexpr (TreeRegs<N>::Values < 80) regs_dec<TreeRegs<N>::Values>();
+    set_regs<R::Launch, R::Values>();
     TokenWalk walk(a, u, t0 + t, t1);
     uint32_t wd[4 * BV], meta;
     int32_t lead;
     uint32_t slot;
     const int64_t vhead = h * L.v_in.head_stride;
-    auto load = [&]() {
-      const int64_t v = lead * L.v_in.unit_stride + vhead + slot;
+    bool held;
+    auto load = [&]() {  // (without a token vector 0, as for the keys)
+      held = lead >= 0;
+      const int64_t v = held ? lead * L.v_in.unit_stride + vhead + slot : 0;
 #pragma unroll
       for (int i = 0; i < BV; ++i) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (lead >= 0) x = __ldg(reinterpret_cast<const uint4*>(L.v_in.codes + v * (4 * BV)) + i);
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(L.v_in.codes + v * (4 * BV)) + i);
         wd[4 * i] = x.x, wd[4 * i + 1] = x.y, wd[4 * i + 2] = x.z, wd[4 * i + 3] = x.w;
       }
-      meta = lead >= 0 ? __ldg(L.v_in.meta + v) : 0u;
+      meta = __ldg(L.v_in.meta + v);
     };
     walk.next(lead, slot);
     load();
@@ -615,6 +650,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
       if (j > 1) tree_wait(bar_o(j), ((j >> 1) - 1) & 1, dead);  // the values of tile j-2 have been read
       float m;
       int e;
+      if (!held) meta = 0u;  // a weight of 0 must meet a finite value
       value_scale(meta, m, e);
       const uint32_t s16 = __half_as_ushort(
           __float2half_rn(__uint_as_float(static_cast<uint32_t>(125 + e) << 23)));
@@ -625,18 +661,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
 #pragma unroll
         for (int i = 0; i < BV; ++i) x[i] = wd[w * BV + i];
         tree_unpack<BV>(x, hh);
-        // byte g of z has coset bit g of these codes in its top bit; a byte
-        // permute that repeats top bits makes the -2^(e-2) lanes of the set groups
-        const uint32_t z = ((meta >> (4 * w)) & 15u) * 0x10204080u;
+        const uint32_t z = coset_bytes(meta >> (4 * w));
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const int ga = tree_slot<BV>(2 * q) >> 3, gb = tree_slot<BV>(2 * q + 1) >> 3;
-          uint32_t m;  // (prmt's sign mode: __byte_perm has no form of it)
-          asm("prmt.b32 %0, %1, %1, %2;"
-              : "=r"(m)
-              : "r"(z), "r"(0x8888u | (ga * 0x11u) | (gb * 0x1100u)));
-          hh[q] = hfma2u(hh[q], ss, neg & m);
-        }
+        for (int q = 0; q < 16; ++q)
+          hh[q] = hfma2u(hh[q], ss, neg & coset_mask(z, tree_slot<BV>(2 * q) >> 3,
+                                                     tree_slot<BV>(2 * q + 1) >> 3));
         const uint32_t dst = base + S::V + (j & 1) * 32768 + (w >> 1) * 16384;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -647,18 +676,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
       warp_arrive(bar_v(j), lane);
       load();
       walk.next(lead, slot);
-      if (lead >= 0) {
-        const int64_t v = lead * L.v_in.unit_stride + vhead + slot;
-        prefetch_l2(L.v_in.codes + v * (4 * BV));
-        prefetch_l2(L.v_in.meta + v);
-      }
     }
-  } else if (warp < 20) {
+  } else if (warp < R::Issue0) {
     // ----------------------------------------------------------- softmax
     // Thread (t, w): token t, query rows HN w .. HN w + HN - 1 of the block.
-    regs_inc<TreeRegs<N>::Softmax>();
+    set_regs<R::Launch, R::Softmax>();
     constexpr int HN = N / 2, CH = HN < 32 ? HN : 32;  // columns; columns at a time
-    const int w = (warp - 12) >> 2, wl = warp & 3;
+    const int w = (warp - R::Softmax0) >> 2, wl = warp & 3;
     const uint32_t bid = 1 + w;  // this warpgroup's named barrier
     float4* fm = reinterpret_cast<float4*>(gen + S::FM) + w * (HN / 2);
     int* wmax = reinterpret_cast<int*>(gen + S::WMax) + w * (HN * 4);
@@ -706,45 +730,62 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
         float top = y[0];
 #pragma unroll
         for (int c = 1; c < CH; ++c) top = fmaxf(top, y[c]);
-        const bool raise = named_bar_or(bid, 128, top > 14.0f || (!started && valid));
-        // the sums are to be rescaled, or weights to be written: O is at rest
-        // and P is free
-        auto o_at_rest = [&]() {
+        const bool raise = named_bar_or(bid, 128, top > kTreeTop || (!started && valid));
+        if (h0 == 0 && j > 1)  // the weights of tile j-2 have been read
+          tree_wait(bar_o(j), ((j >> 1) - 1) & 1, dead);
+        if (raise) {
+          // the sums are to be rescaled: O at rest (the wait above keeps this
+          // barrier from being a phase further)
           if (j > 0) tree_wait(bar_o(j - 1), ((j - 1) >> 1) & 1, dead);
           tc_fence_after();
-        };
-        if (raise) {
-          if (h0 == 0) o_at_rest();
           raised = true;
-          // exact column maxima of the tile, as ordered integers
+          // the columns to move: those past the range, all of them the first time
+          uint32_t cols = 0xFFFFFFFFu;
+          if (started) {
+            cols = 0u;
 #pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            const int i = __float_as_int(y[c]);
-            const int k = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
-            if (lane == 0) wmax[(h0 + c) * 4 + wl] = k;
+            for (int c = 0; c < CH; ++c)
+              if (y[c] > kTreeTop) cols |= 1u << c;
+            cols = __reduce_or_sync(0xffffffffu, cols);
           }
+          uint32_t* wor = reinterpret_cast<uint32_t*>(gen + S::WOr) + w * 4;
+          if (lane == 0) wor[wl] = cols;
+          named_bar_sync(bid, 128);
+          const uint4 o4 = *reinterpret_cast<const uint4*>(wor);
+          cols = (o4.x | o4.y) | (o4.z | o4.w);
+          // their exact maxima over the tile, as ordered integers
+#pragma unroll
+          for (int c = 0; c < CH; ++c)
+            if (cols >> c & 1u) {
+              const int i = __float_as_int(y[c]);
+              const int k = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
+              if (lane == 0) wmax[(h0 + c) * 4 + wl] = k;
+            }
           named_bar_sync(bid, 128);
           auto delta_of = [&](int c) {
             const int4 k4 = *reinterpret_cast<const int4*>(wmax + c * 4);
             const int k = max(max(k4.x, k4.y), max(k4.z, k4.w));
-            const float d = __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)) - 6.0f;
-            return started ? fmaxf(d, 0.f) : d;
+            return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)) - kTreeStart;
           };
-          if (t < CH) {
+          if (t < CH && (cols >> t & 1u)) {
             float* m = reinterpret_cast<float*>(fm + ((h0 + t) >> 1)) + 2 + (t & 1);
             *m -= delta_of(h0 + t);
           }
 #pragma unroll
           for (int c0 = 0; c0 < CH; c0 += 4) {
+            if ((cols >> c0 & 15u) == 0u) continue;
             float al[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const float d = delta_of(h0 + c0 + c);
-              y[c0 + c] -= d;
-              al[c] = ex2(-d);
-              l[h0 + c0 + c] = started ? l[h0 + c0 + c] * al[c] : 0.f;
+              al[c] = 1.0f;
+              if (cols >> (c0 + c) & 1u) {
+                const float d = delta_of(h0 + c0 + c);
+                y[c0 + c] -= d;
+                al[c] = started ? ex2(-d) : 0.f;
+                l[h0 + c0 + c] *= al[c];
+              }
             }
-            if (started && j > 0) {
+            if (started) {
               uint32_t o[4];
               tmem_ld(tO + t_lane + w * HN + h0 + c0, o);
               tmem_wait_ld(o);
@@ -767,18 +808,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
           const __half2 ph = __floats2half2_rn(pm.x, pm.y);
           pk[c / 2] = *reinterpret_cast<const uint32_t*>(&ph);
         }
-        if (h0 == 0 && !raise) o_at_rest();
 #pragma unroll
         for (int c = 0; c < CH; c += 8) {
           const int col = w * HN + h0 + c;
-          sts128(base + S::P + (col / 64) * 16384 + row_chunk(t, (col % 64) >> 3),
+          sts128(base + S::P + (j & 1) * S::PBytes + (col / 64) * 16384 + row_chunk(t, (col % 64) >> 3),
                  make_uint4(pk[c / 2], pk[c / 2 + 1], pk[c / 2 + 2], pk[c / 2 + 3]));
         }
       }
       started = started || raised;
       fence_proxy_async_smem();
       tc_fence_before();
-      warp_arrive(bar_p, lane);
+      warp_arrive(bar_p(j), lane);
     }
     tree_wait(bar_o(nt - 1), ((nt - 1) >> 1) & 1, dead);
     tc_fence_after();
@@ -815,46 +855,44 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
     tc_fence_before();
   } else {
     // ---------------------------------------------------------- the MMAs
-    regs_dec<TreeRegs<N>::Issue>();
+    set_regs<R::Launch, R::Issue>();
     // low words of the matrix descriptors (address >> 4, leading offset above
     // bit 16), so that an instruction costs one addition per operand
     const uint32_t b4 = base >> 4;
-    constexpr uint32_t iX = idesc_f16_f32(128, 64), iC = idesc_f16_f32(128, 128);
+    constexpr uint32_t iX = idesc_f16_f32(128, 64);
     constexpr uint32_t iS = idesc_f16_f32(128, N), iO = idesc_f16_f32(128, N) | kIdescAMn | kIdescBMn;
     const uint32_t one = elect_lane();
     // two tiles per round, so that everything that an instruction names by
     // the tile's parity is a constant
-    if (warp == 20) {  // X = t H
+    if (warp == R::Issue0) {  // X = t H
       auto step = [&](int j, auto parity) {
-        constexpr uint32_t d = kTmX + decltype(parity)::value * 128;
+        constexpr uint32_t d = S::tX + (decltype(parity)::value % S::XBufs) * 128;
         tree_wait(bar_t, j & 1, dead);
+        if (S::XBufs == 1 && j > 0) tree_wait(bar_xf, (j - 1) & 1, dead);
         tc_fence_after();
-        umma_f16_if(one, d, desc_plain(base + S::CA, 2048, 128), desc_plain(base + S::CB, 2048, 128),
-                    iC, 0u);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_f16_if(one, d + 64 * hf, tree_desc(b4 + ((S::T + hf * 16384 + k * 32) >> 4), 1u),
-                        tree_desc(b4 + ((S::H + k * 32) >> 4), 1u), iX, 1u);
+            umma_f16_ta_if(one, d + 64 * hf, S::tT + 32 * hf + 8 * k,
+                           tree_desc(b4 + ((S::H + k * 32) >> 4), 1u), iX, k > 0);
         umma_commit_if(one, bar_x);
       };
       for (int j = 0; j < nt; j += 2) {
         step(j, Parity<0>());
         if (j + 1 < nt) step(j + 1, Parity<1>());
       }
-    } else if (warp == 21) {  // S = keys Q^T
+    } else if (warp == R::Issue0 + 1) {  // S = keys Q^T
       auto step = [&](int j, auto parity) {
         constexpr int q = decltype(parity)::value;
         tree_wait(bar_k(q), (j >> 1) & 1, dead);
         if (j > 0) tree_wait(bar_sf, (j - 1) & 1, dead);
         tc_fence_after();
-        constexpr uint32_t kb = S::K + (q % S::KBufs) * 32768;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          umma_f16_if(one, kTmS, tree_desc(b4 + ((kb + (k >> 2) * 16384 + (k & 3) * 32) >> 4), 1u),
-                      tree_desc(b4 + ((S::Q + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), 1u), iS,
-                      k > 0);
+          umma_f16_ta_if(one, tS, S::tK + (q % S::KBufs) * 64 + 8 * k,
+                         tree_desc(b4 + ((S::Q + (k >> 2) * (N * 128) + (k & 3) * 32) >> 4), 1u), iS,
+                         k > 0);
         umma_commit_if(one, bar_s(q));
         // orders the key scales, which this warp's wait for the keys has
         // acquired, before the softmax threads' reads
@@ -865,17 +903,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
         step(j, Parity<0>());
         if (j + 1 < nt) step(j + 1, Parity<1>());
       }
-    } else if (warp == 22) {  // O += V P
+    } else if (warp == R::Issue0 + 2) {  // O += V P
       auto step = [&](int j, auto parity) {
         constexpr int q = decltype(parity)::value;
         tree_wait(bar_v(q), (j >> 1) & 1, dead);
-        tree_wait(bar_p, j & 1, dead);
+        tree_wait(bar_p(q), (j >> 1) & 1, dead);
         tc_fence_after();
         const uint32_t more = j > 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          umma_f16_if(one, kTmS + N, tree_desc(b4 + ((S::V + q * 32768 + k * 2048) >> 4), 16384u >> 4),
-                      tree_desc(b4 + ((S::P + k * 2048) >> 4), 16384u >> 4), iO, k > 0 ? 1u : more);
+          umma_f16_if(one, tO, tree_desc(b4 + ((S::V + q * 32768 + k * 2048) >> 4), 16384u >> 4),
+                      tree_desc(b4 + ((S::P + q * S::PBytes + k * 2048) >> 4), 16384u >> 4), iO,
+                      k > 0 ? 1u : more);
         umma_commit_if(one, bar_o(q));
       };
       for (int j = 0; j < nt; j += 2) {
@@ -885,9 +924,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_partial_kernel(const Tre
     }
   }
   __syncthreads();
-  if (warp == 20) {
+  if (warp == R::Issue0) {
     tc_fence_after();
-    tmem_dealloc(tmem, kCols);
+    tmem_dealloc(0u, kCols);
   }
 }
 
@@ -1027,7 +1066,7 @@ static cudaError_t launch_tree_n(const TreeArgs& a, int64_t grid, cudaStream_t s
   cudaError_t err = cudaFuncSetAttribute(tree_partial_kernel<BK, BV, N>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  tree_partial_kernel<BK, BV, N><<<static_cast<unsigned>(grid), kTreeThreads, smem, stream>>>(a);
+  tree_partial_kernel<BK, BV, N><<<static_cast<unsigned>(grid), TreeRoles<N>::Threads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 

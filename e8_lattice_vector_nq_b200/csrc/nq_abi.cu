@@ -708,9 +708,9 @@ nq_status nq_encode_slots(const void* K, nq_kv_strides ks, const void* V, nq_kv_
 }
 
 size_t nq_tree_attend_workspace_bytes(int units, int heads, int G, int nodes, int64_t n,
-                                      int shared) {
-  if (units < 0 || heads < 1 || G < 1 || nodes < 1 || n < 1) return 0;
-  return nq::tree_workspace_bytes(units, heads, G, nodes, n, shared != 0);
+                                      int shared, int ragged) {
+  if (units < 1 || heads < 1 || G < 1 || nodes < 1 || n < 1) return 0;
+  return nq::tree_workspace_bytes(units, heads, G, nodes, n, shared != 0, ragged != 0);
 }
 
 nq_status nq_tree_attend(const void* q, nq_kv_strides qs, const void* K_new, nq_kv_strides kns,
@@ -729,6 +729,8 @@ nq_status nq_tree_attend(const void* q, nq_kv_strides qs, const void* K_new, nq_
   if (n < 0 || pos_base < 0) return fail(NQ_ERR_INVALID, "need n >= 0, pos_base >= 0");
   if (!std::isfinite(scale)) return fail(NQ_ERR_INVALID, "scale must be finite");
   if (units == 0) return NQ_OK;
+  if (static_cast<int64_t>(units) * heads * G * nodes > 0x7FFFFFFF)
+    return fail(NQ_ERR_UNSUPPORTED, "units * heads * G * nodes must stay below 2^31");
   if (nq_status st = check_kv(q, qs, "q")) return st;
   if (nq_status st = check_kv(K_new, kns, "K_new")) return st;
   if (nq_status st = check_kv(V_new, vns, "V_new")) return st;
@@ -764,17 +766,16 @@ nq_status nq_tree_attend(const void* q, nq_kv_strides qs, const void* K_new, nq_
                     static_cast<long long>(table_stride));
     }
     if (n > 0x7FFFFFFF || pos_base + n > 0x7FFFFFFF ||
-        nq::tree_ctas(units, heads, G, nodes, n) > 0x7FFFFFFF)
+        nq::tree_ctas(units, heads, G, nodes, n, lens != nullptr) > 0x7FFFFFFF)
       return fail(NQ_ERR_UNSUPPORTED, "n or units * heads * chunks too large for one launch");
     if (!ws || !aligned(ws, 16))
       return fail(NQ_ERR_INVALID, "workspace NULL or not 16-byte aligned");
     const size_t need =
-        nq_tree_attend_workspace_bytes(units, heads, G, nodes, n, positions == nullptr);
+        nq_tree_attend_workspace_bytes(units, heads, G, nodes, n, positions == nullptr,
+                                       lens != nullptr);
     if (ws_bytes < need)
       return fail(NQ_ERR_WORKSPACE, "tree attention workspace too small: %zu < %zu", ws_bytes, need);
   }
-  if (static_cast<int64_t>(units) * heads * G * nodes > 0x7FFFFFFF)
-    return fail(NQ_ERR_UNSUPPORTED, "units * heads * G * nodes must stay below 2^31");
   nq::TreeLaunch L{};
   L.q = q;
   L.qs = qs;

@@ -164,8 +164,9 @@ cudaError_t launch_decode(const DecodeLaunch& L, cudaStream_t stream);
 cudaError_t launch_encode_slots(const EncodeSlotsLaunch& L, cudaStream_t stream);
 cudaError_t launch_page_tables(const PageTablesLaunch& L, cudaStream_t stream);
 cudaError_t launch_norm_rope(const NormRopeLaunch& L, cudaStream_t stream);
-size_t tree_workspace_bytes(int units, int heads, int G, int nodes, int64_t n, bool shared);
-int64_t tree_ctas(int units, int heads, int G, int nodes, int64_t n);  // of its largest launch
+size_t tree_workspace_bytes(int units, int heads, int G, int nodes, int64_t n, bool shared,
+                            bool ragged);
+int64_t tree_ctas(int units, int heads, int G, int nodes, int64_t n, bool ragged);  // of its largest launch
 cudaError_t tree_read_clear_error(uint32_t* flags);  // after a synchronisation
 cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream);
 

@@ -260,7 +260,7 @@ __device__ __forceinline__ void load_weight(const float* w, int l, float (&g)[16
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, 3) norm_rope_kernel(const NormArgs a) {
   const NormRopeLaunch& L = a.L;
   const int l = threadIdx.x & 7;
   const int64_t item = (static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x) >> 3;
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormArgs 
   load_weight(h0 < L.q_heads ? L.q_weight : L.k_weight, l, g);
   // the groups of a warp may run different numbers of heads: each shuffles alone
   const uint32_t lanes = 0xFFu << (threadIdx.x & 24);
-  constexpr int kU = F32 ? 2 : 4;  // heads whose loads are in flight together
+  constexpr int kU = 2;  // heads whose loads are in flight together
   for (int h = h0; h < h1; h += kU) {
     float x[kU][16];
 #pragma unroll

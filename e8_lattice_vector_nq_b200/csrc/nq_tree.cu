@@ -21,11 +21,12 @@
 //      = 2^e m, so V' is exact and a token's weight is rounded once (no
 //      transform: the codes' coordinates are summed, and H is applied once per
 //      row at the end).
-// m_r is not the running maximum but a reference kept within 2^8 of it: p
-// starts at 2^6 and stays below 2^14, so the maximum may grow by 2^8 before
-// the sums are rescaled, and f16 holds p down to 2^-30 of the maximum.  A tile whose
-// scores leave that range (the first one always) takes the exact column
-// maxima; the others only compare (one vote per tile and warpgroup).
+// m_r is not the running maximum but a reference kept near it: a column's
+// largest p starts at 2^4 and stays below 2^14, so the maximum may grow by
+// 2^10 before the sums are rescaled, and f16 holds p down to 2^-28 of the
+// maximum.  A tile whose scores leave that range (the first one always) takes
+// the exact maxima of those columns; the others only compare (one vote per
+// tile and warpgroup).
 //
 // One CTA per SM, its warpgroups specialised so that the phases of different
 // tiles overlap: two or four warpgroups make keys (a token per thread and a
@@ -50,8 +51,9 @@ namespace nq {
 
 constexpr int kTreeTile = 128;     // tokens per tile
 constexpr int kTreePart = 2 + kD;  // a split's m (log2 units), l, sums[128] in the code domain
-constexpr float kTreeStart = 4.0f, kTreeTop = 14.0f;  // log2 of a column's largest weight: see below
+constexpr float kTreeStart = 4.0f, kTreeTop = 14.0f;  // log2 of a column's largest weight
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTreeMaxSplits = 4 * 148;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kTreeWaitLimit = 1u << 16, kTreeWaitNs = 16384;  // about a second
 constexpr uint32_t kErrTreeTimeout = 4u;
@@ -78,41 +80,55 @@ __device__ __forceinline__ int64_t tree_len(const TreeLaunch& L, int64_t u) {
 }
 
 // ------------------------------------------------------------------ angles
-// Thread (t, w) of a tile: c' = c - s and s' = c + s of its token at the
-// frequencies 16w .. 16w+15, entry x holding frequencies 16w+4x .. +3 as
-// (c' pair, s' pair, c' pair, s' pair).
-__global__ void __launch_bounds__(512) tree_angles_kernel(const TreeArgs a) {
-  const int t = threadIdx.x & 127, w = threadIdx.x >> 7;
+// Per token c' = c - s and s' = c + s of the 64 frequencies as f16 pairs:
+// entry e (16 bytes) holds frequencies 4e .. 4e+3 as (c' pair, s' pair, c'
+// pair, s' pair), the 128 tokens of a tile side by side.  A warp reads each
+// token's two table rows whole (lane l: frequencies 2l, 2l+1) and the tile
+// goes through shared memory, so that both sides are contiguous.
+constexpr int kAngleThreads = 256;
+constexpr int kAnglePitch = 256 + 16;  // bytes per token: neither side has bank conflicts
+__global__ void __launch_bounds__(kAngleThreads) tree_angles_kernel(const TreeArgs a) {
+  __shared__ __align__(16) unsigned char rows[kTreeTile * kAnglePitch];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t tile = blockIdx.x % a.tiles, u = blockIdx.x / a.tiles;
-  const int64_t tok = tile * kTreeTile + t;
-  int64_t pos = 0;
-  if (tok < a.L.n) {
-    const int32_t p = a.L.positions ? __ldg(a.L.positions + u * a.L.pos_stride + tok)
-                                    : static_cast<int32_t>(tok);
-    pos = a.L.pos_base + (p < 0 ? 0 : p);  // out-of-contract positions stay in bounds
-  }
-  int64_t hi = pos >> 8;
-  hi = hi >= a.n_a ? a.n_a - 1 : hi;
-  const float4* ra = reinterpret_cast<const float4*>(a.L.rope_tab) + hi * (kHalf / 2) + 8 * w;
-  const float4* rb =
-      reinterpret_cast<const float4*>(a.L.rope_tab) + (a.n_a + (pos & 255)) * (kHalf / 2) + 8 * w;
-  uint4* out = a.angles + u * a.angle_stride + ((tile * 4 + w) * 4) * 128 + t;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    uint32_t e[4];
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const float4 A = __ldg(ra + 2 * x + y), B = __ldg(rb + 2 * x + y);
-      const float c0 = __fmaf_rn(A.x, B.x, -__fmul_rn(A.y, B.y));
-      const float s0 = __fmaf_rn(A.y, B.x, __fmul_rn(A.x, B.y));
-      const float c1 = __fmaf_rn(A.z, B.z, -__fmul_rn(A.w, B.w));
-      const float s1 = __fmaf_rn(A.w, B.z, __fmul_rn(A.z, B.w));
-      const __half2 cc = __floats2half2_rn(c0 - s0, c1 - s1);
-      const __half2 ss = __floats2half2_rn(c0 + s0, c1 + s1);
-      e[2 * y] = *reinterpret_cast<const uint32_t*>(&cc);
-      e[2 * y + 1] = *reinterpret_cast<const uint32_t*>(&ss);
+  constexpr int kPer = kTreeTile / (kAngleThreads / 32);  // tokens per warp
+  const int first = warp * kPer;
+  int64_t mine = 0;  // lane l: the position of the warp's token l
+  {
+    const int64_t tok = tile * kTreeTile + first + lane;
+    if (lane < kPer && tok < a.L.n) {
+      const int32_t p = a.L.positions ? __ldg(a.L.positions + u * a.L.pos_stride + tok)
+                                      : static_cast<int32_t>(tok);
+      mine = a.L.pos_base + (p < 0 ? 0 : p);  // out-of-contract positions stay in bounds
     }
-    out[x * 128] = make_uint4(e[0], e[1], e[2], e[3]);
+  }
+  const float4* tab = reinterpret_cast<const float4*>(a.L.rope_tab);
+  const int pos32 = static_cast<int>(mine);  // below 2^31: the ABI layer checks
+  // nearby positions share the coarse row: it is read again only when it changes
+  int64_t row = -1;
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < kPer; ++i) {
+    const int pos = __shfl_sync(0xffffffffu, pos32, i);
+    const float4 B = __ldg(tab + (a.n_a + (pos & 255)) * 32 + lane);
+    const int64_t hi = min64(pos >> 8, a.n_a - 1);
+    if (hi != row) A = __ldg(tab + hi * 32 + lane);
+    row = hi;
+    const float c0 = __fmaf_rn(A.x, B.x, -__fmul_rn(A.y, B.y));
+    const float s0 = __fmaf_rn(A.y, B.x, __fmul_rn(A.x, B.y));
+    const float c1 = __fmaf_rn(A.z, B.z, -__fmul_rn(A.w, B.w));
+    const float s1 = __fmaf_rn(A.w, B.z, __fmul_rn(A.z, B.w));
+    const __half2 cc = __floats2half2_rn(c0 - s0, c1 - s1);
+    const __half2 ss = __floats2half2_rn(c0 + s0, c1 + s1);
+    *reinterpret_cast<uint2*>(rows + (first + i) * kAnglePitch + lane * 8) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&cc), *reinterpret_cast<const uint32_t*>(&ss));
+  }
+  __syncthreads();
+  uint4* out = a.angles + u * a.angle_stride + tile * (16 * kTreeTile);
+#pragma unroll
+  for (int i = 0; i < 16 * kTreeTile / kAngleThreads; ++i) {
+    const int e = (i * kAngleThreads + threadIdx.x) >> 7, t = threadIdx.x & 127;
+    out[e * kTreeTile + t] = *reinterpret_cast<const uint4*>(rows + t * kAnglePitch + e * 16);
   }
 }
 
@@ -225,6 +241,27 @@ __device__ __forceinline__ void tree_unpack(const uint32_t (&w)[BITS], uint32_t 
 // output row per row; MN-major: a token, the k index, per row).
 __device__ __forceinline__ uint32_t row_chunk(int t, int c) {
   return static_cast<uint32_t>((t >> 3) * 1024 + (t & 7) * 128 + ((c ^ (t & 7)) << 4));
+}
+
+// The reduction over the warp's lanes of each of C columns (C a power of two
+// up to 32) that every lane holds a value of: lane c (mod C) returns column
+// c's.  Each step halves the columns that a lane carries, so C columns take
+// about C shuffles instead of 5 C.
+template <int C, class F>
+__device__ __forceinline__ float column_reduce(float (&x)[C], int lane, F f) {
+#pragma unroll
+  for (int o = C / 2; o >= 1; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int c = 0; c < o; ++c) {
+      const float keep = up ? x[c + o] : x[c], give = up ? x[c] : x[c + o];
+      x[c] = f(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  float v = x[0];
+#pragma unroll
+  for (int o = 16; o >= C; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -427,6 +464,19 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
     *dead = 0u;
     fence_mbar_init();
   }
+  constexpr int kRows = (N + R::Threads / 32 - 1) / (R::Threads / 32);  // query rows per warp
+  uint2 qv[kRows];  // all of the warp's rows in flight together
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp + i * (R::Threads / 32), row = row0 + r;
+    qv[i] = make_uint2(0u, 0u);
+    if (r < N && row < a.rows) {
+      const int node = row / L.G, j = h * L.G + row % L.G;
+      qv[i] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(L.q) +
+                                                   u * L.qs.unit + j * L.qs.head +
+                                                   node * L.qs.token) + lane);
+    }
+  }
   if (tid < 512) {  // H64: row n, chunk c (8 slots)
     const int n = tid >> 3, c = tid & 7;
     uint32_t v[4];
@@ -443,19 +493,11 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
     }
     sts128(base + S::H + row_chunk(n, c), make_uint4(v[0], v[1], v[2], v[3]));
   }
-  for (int r = warp; r < N; r += R::Threads / 32) {
-    const int row = row0 + r;
-    float q[4] = {0.f, 0.f, 0.f, 0.f};
-    if (row < a.rows) {
-      const int node = row / L.G, j = h * L.G + row % L.G;
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(L.q) +
-                                                           u * L.qs.unit + j * L.qs.head +
-                                                           node * L.qs.token) + lane);
-      q[0] = bf16lo(v.x);
-      q[1] = bf16hi(v.x);
-      q[2] = bf16lo(v.y);
-      q[3] = bf16hi(v.y);
-    }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp + i * (R::Threads / 32);
+    if (r >= N) break;
+    const float q[4] = {bf16lo(qv[i].x), bf16hi(qv[i].x), bf16lo(qv[i].y), bf16hi(qv[i].y)};
     float m = fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])));
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -478,10 +520,13 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
       fm[2] = 0.f;
     }
   }
-  fence_proxy_async_smem();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  // every role calls this once, the loading ones after their first loads
+  auto setup_done = [&]() {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  };
   // the whole of TMEM is allocated (512 columns), so it starts at column 0
   constexpr uint32_t tS = S::tS, tO = S::tO;
   const int t = tid & 127;
@@ -567,6 +612,7 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
     walk.next(lead, slot);
     load();
     walk.next(lead, slot);
+    setup_done();
     write_t(0);
     for (int j = 0; j < nt; ++j) {
       // the angles of two runs of frequencies, those of the next two follow
@@ -646,6 +692,7 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
     walk.next(lead, slot);
     load();
     walk.next(lead, slot);
+    setup_done();
     for (int j = 0; j < nt; ++j) {
       if (j > 1) tree_wait(bar_o(j), ((j >> 1) - 1) & 1, dead);  // the values of tile j-2 have been read
       float m;
@@ -680,6 +727,7 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
   } else if (warp < R::Issue0) {
     // ----------------------------------------------------------- softmax
     // Thread (t, w): token t, query rows HN w .. HN w + HN - 1 of the block.
+    setup_done();
     set_regs<R::Launch, R::Softmax>();
     constexpr int HN = N / 2, CH = HN < 32 ? HN : 32;  // columns; columns at a time
     const int w = (warp - R::Softmax0) >> 2, wl = warp & 3;
@@ -733,21 +781,41 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
         const bool raise = named_bar_or(bid, 128, top > kTreeTop || (!started && valid));
         if (h0 == 0 && j > 1)  // the weights of tile j-2 have been read
           tree_wait(bar_o(j), ((j >> 1) - 1) & 1, dead);
-        if (raise) {
+        if (raise && !started) {
+          // the first tokens of the split: every column's exact maximum (lane c
+          // of a warp: column h0 + c), before which the references are 0
+          raised = true;
+          float x[CH];
+#pragma unroll
+          for (int c = 0; c < CH; ++c) x[c] = y[c];
+          const float k = column_reduce<CH>(x, lane, [](float p, float q) { return fmaxf(p, q); });
+          float* fmax4 = reinterpret_cast<float*>(wmax);
+          if (lane < CH) fmax4[(h0 + lane) * 4 + wl] = k;
+          named_bar_sync(bid, 128);
+          if (wl == 0 && lane < CH) {
+            const float4 k4 = *reinterpret_cast<const float4*>(fmax4 + (h0 + lane) * 4);
+            float* m = reinterpret_cast<float*>(fm + ((h0 + lane) >> 1)) + 2 + (lane & 1);
+            *m = kTreeStart - fmaxf(fmaxf(k4.x, k4.y), fmaxf(k4.z, k4.w));
+          }
+          named_bar_sync(bid, 128);  // the references are written, wmax is free
+#pragma unroll
+          for (int c = 0; c < CH; c += 2) {
+            const float4 f = fm[(h0 + c) / 2];
+            y[c] += f.z;
+            y[c + 1] += f.w;
+          }
+        } else if (raise) {
           // the sums are to be rescaled: O at rest (the wait above keeps this
           // barrier from being a phase further)
           if (j > 0) tree_wait(bar_o(j - 1), ((j - 1) >> 1) & 1, dead);
           tc_fence_after();
           raised = true;
-          // the columns to move: those past the range, all of them the first time
-          uint32_t cols = 0xFFFFFFFFu;
-          if (started) {
-            cols = 0u;
+          // the columns to move: those past the range
+          uint32_t cols = 0u;
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
-              if (y[c] > kTreeTop) cols |= 1u << c;
-            cols = __reduce_or_sync(0xffffffffu, cols);
-          }
+          for (int c = 0; c < CH; ++c)
+            if (y[c] > kTreeTop) cols |= 1u << c;
+          cols = __reduce_or_sync(0xffffffffu, cols);
           uint32_t* wor = reinterpret_cast<uint32_t*>(gen + S::WOr) + w * 4;
           if (lane == 0) wor[wl] = cols;
           named_bar_sync(bid, 128);
@@ -781,18 +849,16 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
               if (cols >> (c0 + c) & 1u) {
                 const float d = delta_of(h0 + c0 + c);
                 y[c0 + c] -= d;
-                al[c] = started ? ex2(-d) : 0.f;
+                al[c] = ex2(-d);
                 l[h0 + c0 + c] *= al[c];
               }
             }
-            if (started) {
-              uint32_t o[4];
-              tmem_ld(tO + t_lane + w * HN + h0 + c0, o);
-              tmem_wait_ld(o);
+            uint32_t o[4];
+            tmem_ld(tO + t_lane + w * HN + h0 + c0, o);
+            tmem_wait_ld(o);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
-              tmem_st(tO + t_lane + w * HN + h0 + c0, o);
-            }
+            for (int c = 0; c < 4; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
+            tmem_st(tO + t_lane + w * HN + h0 + c0, o);
           }
           tmem_wait_st();
           named_bar_sync(bid, 128);  // the references are written, wmax is free
@@ -825,6 +891,8 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
 
     // ---- the split's sums: lane = code coordinate of this thread's TMEM lane
     const int coord = 32 * (t >> 5) + tree_slot<BV>(t & 31);
+    float* out = part + w * HN * part_row + 2 + coord;
+    const int left = a.rows - row0 - w * HN;  // rows of this half that exist
 #pragma unroll
     for (int c0 = 0; c0 < HN; c0 += 8) {
       uint32_t o[8];
@@ -832,17 +900,18 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
       tmem_wait_ld(o);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const int r = w * HN + c0 + c;
-        if (row0 + r < a.rows) part[r * part_row + 2 + coord] = __uint_as_float(o[c]);
+        if (c0 + c < left) *out = __uint_as_float(o[c]);
+        out += part_row;
       }
     }
     float* wsum = reinterpret_cast<float*>(wmax);
 #pragma unroll
-    for (int c = 0; c < HN; ++c) {
-      float s = l[c];
+    for (int c0 = 0; c0 < HN; c0 += CH) {
+      float x[CH];
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0) wsum[c * 4 + wl] = s;
+      for (int c = 0; c < CH; ++c) x[c] = l[c0 + c];
+      const float k = column_reduce<CH>(x, lane, [](float p, float q) { return p + q; });
+      if (lane < CH) wsum[(c0 + lane) * 4 + wl] = k;
     }
     named_bar_sync(bid, 128);
     if (t < HN && row0 + w * HN + t < a.rows) {
@@ -855,6 +924,7 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
     tc_fence_before();
   } else {
     // ---------------------------------------------------------- the MMAs
+    setup_done();
     set_regs<R::Launch, R::Issue>();
     // low words of the matrix descriptors (address >> 4, leading offset above
     // bit 16), so that an instruction costs one addition per operand
@@ -930,83 +1000,155 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
   }
 }
 
-// One warp per row: merge the splits, transform, then attend the draft nodes
-// that the row sees one by one (fp32).  Lane l holds coordinates l, l+32,
-// l+64, l+96: Hadamard stages 1..16 across lanes, 32 and 64 in the lane.
-__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a) {
+// One warp per row: merge the splits, apply H, attend the draft nodes that
+// the row sees (fp32).  Lane l owns coordinates l, l+32, l+64, l+96; a draft
+// score takes eight lanes (16 coordinates each).  Latency counts here: the
+// loads of a phase are independent of each other.
+constexpr int kCombineWarps = 4;
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Shared floats of a warp: split factors, draft scores (then weights, 0: not
+// seen), the query.
+__host__ __device__ constexpr int combine_floats(int nsplit, int nodes) {
+  return (nsplit + nodes + 3) / 4 * 4 + kD;  // the query 16-byte aligned
+}
+
+__global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const TreeArgs a) {
+  extern __shared__ float combine_smem[];
   const TreeLaunch& L = a.L;
   const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
   if (w >= static_cast<int64_t>(L.units) * L.heads * a.rows) return;
+  const int ns = static_cast<int>(a.nsplit);
+  float* fac = combine_smem + (threadIdx.x >> 5) * combine_floats(ns, L.nodes);
+  float* sc = fac + ns;
+  float* qs = fac + combine_floats(ns, L.nodes) - kD;
   const int r = static_cast<int>(w % a.rows);
   const int64_t uh = w / a.rows, u = uh / L.heads;
   const int h = static_cast<int>(uh % L.heads), node = r / L.G, j = h * L.G + r % L.G;
   const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(L.q) + u * L.qs.unit +
                             j * L.qs.head + node * L.qs.token;
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) q[c] = __bfloat162float(qp[lane + 32 * c]) * (L.scale * kLog2e);
-  const float* p0 = a.part + w * a.nsplit * kTreePart;
-  for (int64_t s = 0; s < a.nsplit; ++s) m = fmaxf(m, p0[s * kTreePart]);
-  if (m > -INFINITY) {
-    for (int64_t s = 0; s < a.nsplit; ++s) {
-      const float* p = p0 + s * kTreePart;
-      if (p[0] == -INFINITY) continue;  // no token in it: its sums were not written
-      const float f = exp2f(p[0] - m);
-      l = __fmaf_rn(f, p[1], l);
+  for (int i = 0; i < 4; ++i)
+    qs[lane + 32 * i] = __bfloat162float(qp[lane + 32 * i]) * (L.scale * kLog2e);
+  const float* part = a.part + w * a.nsplit * kTreePart;
+  float top = -INFINITY;
+  for (int s = lane; s < ns; s += 32) {
+    const float m = part[static_cast<int64_t>(s) * kTreePart];
+    fac[s] = m;
+    top = fmaxf(top, m);
+  }
+  __syncwarp();
+
+  // draft scores, four nodes at a time
+  const int words = (L.nodes + 63) / 64;
+  const unsigned long long* mask =
+      L.mask ? reinterpret_cast<const unsigned long long*>(L.mask) + u * L.mask_stride +
+                   static_cast<int64_t>(node) * words
+             : nullptr;
+  const int last = mask ? L.nodes : node + 1;  // a chain sees nodes 0 .. node
+  const __nv_bfloat16* Kn = static_cast<const __nv_bfloat16*>(L.K_new) + u * L.kns.unit + h * L.kns.head;
+  const __nv_bfloat16* Vn = static_cast<const __nv_bfloat16*>(L.V_new) + u * L.vns.unit + h * L.vns.head;
+#pragma unroll 2
+  for (int k0 = 0; k0 < last; k0 += 4) {
+    const int k = k0 + (lane >> 3), e = lane & 7;  // lane e: coordinates 8e .. +7, 64 + 8e .. +7
+    const bool seen = k < last && (!mask || (__ldg(mask + (k >> 6)) >> (k & 63) & 1ull));
+    float s = 0.f;
+    if (seen) {
+      const uint4* src = reinterpret_cast<const uint4*>(Kn + k * L.kns.token);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[c] = __fmaf_rn(f, p[2 + lane + 32 * c], o[c]);
-    }
-#pragma unroll
-    for (int st = 1; st < 32; st <<= 1) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float x = __shfl_xor_sync(0xffffffffu, o[c], st);
-        o[c] = (lane & st) ? x - o[c] : o[c] + x;
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint4 v = __ldg(src + 8 * hf + e);
+        const float4 q0 = *reinterpret_cast<const float4*>(qs + 64 * hf + 8 * e);
+        const float4 q1 = *reinterpret_cast<const float4*>(qs + 64 * hf + 8 * e + 4);
+        s = __fmaf_rn(bf16lo(v.x), q0.x, s);
+        s = __fmaf_rn(bf16hi(v.x), q0.y, s);
+        s = __fmaf_rn(bf16lo(v.y), q0.z, s);
+        s = __fmaf_rn(bf16hi(v.y), q0.w, s);
+        s = __fmaf_rn(bf16lo(v.z), q1.x, s);
+        s = __fmaf_rn(bf16hi(v.z), q1.y, s);
+        s = __fmaf_rn(bf16lo(v.w), q1.z, s);
+        s = __fmaf_rn(bf16hi(v.w), q1.w, s);
       }
     }
-    // the sums are of sigma t / 4: v = (sigma / 2) C H t
-    const float k = 2.0f * __uint_as_float(kCBits);
-    const float x0 = (o[0] + o[1]) * k, x1 = (o[0] - o[1]) * k;
-    const float x2 = (o[2] + o[3]) * k, x3 = (o[2] - o[3]) * k;
-    o[0] = x0 + x2;
-    o[2] = x0 - x2;
-    o[1] = x1 + x3;
-    o[3] = x1 - x3;
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (k < last && e == 0) sc[k] = seen ? s : -INFINITY;
+    if (seen) top = fmaxf(top, s);
   }
-  const int words = (L.nodes + 63) / 64;
-  for (int x = 0; x < words; ++x) {
-    const int left = L.mask ? L.nodes - 64 * x : node + 1 - 64 * x;
-    unsigned long long bits = left >= 64 ? ~0ull : (left <= 0 ? 0ull : (1ull << left) - 1);
-    if (L.mask) bits &= L.mask[u * L.mask_stride + static_cast<int64_t>(node) * words + x];
-    while (bits) {
-      const int k = 64 * x + __ffsll(static_cast<long long>(bits)) - 1;
-      bits &= bits - 1;
-      const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(L.K_new) + u * L.kns.unit +
-                                h * L.kns.head + k * L.kns.token;
-      const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(L.V_new) + u * L.vns.unit +
-                                h * L.vns.head + k * L.vns.token;
-      float s = 0.f;
+
+  // the common reference of the splits and the draft, then the factors
+  const float M = warp_max(top), ref = M == -INFINITY ? 0.f : M;
+  __syncwarp();
+  float l = 0.f;
+  for (int s = lane; s < ns; s += 32) {
+    const float f = exp2f(fac[s] - ref);  // 0 for a split without tokens
+    fac[s] = f;
+    if (f > 0.f) l = __fmaf_rn(f, part[static_cast<int64_t>(s) * kTreePart + 1], l);
+  }
+  for (int k = lane; k < last; k += 32) {
+    const float p = exp2f(sc[k] - ref);
+    sc[k] = p;
+    l += p;
+  }
+  const float sum = warp_sum(l);
+  __syncwarp();
+
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < ns; ++s) {
+    const float f = fac[s];
+    if (f > 0.f) {
+      const float* p = part + static_cast<int64_t>(s) * kTreePart + 2 + lane;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s = __fmaf_rn(q[c], __bfloat162float(kp[lane + 32 * c]), s);
-#pragma unroll
-      for (int x2 = 16; x2 >= 1; x2 >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x2);
-      const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2f(m - ref), g = exp2f(s - ref);
-      l = __fmaf_rn(l, f, g);
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        o[c] = __fmaf_rn(o[c], f, g * __bfloat162float(vp[lane + 32 * c]));
-      m = mn;
+      for (int i = 0; i < 4; ++i) o[i] = __fmaf_rn(f, p[32 * i], o[i]);
     }
   }
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
+  // H: stages 1 .. 16 across lanes, 32 and 64 in the lane
+#pragma unroll
+  for (int st = 1; st < 32; st <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = __shfl_xor_sync(0xffffffffu, o[i], st);
+      o[i] = (lane & st) ? x - o[i] : o[i] + x;
+    }
+  }
+  // the sums are of sigma t / 4: v = (sigma / 2) C H t
+  const float kv = 2.0f * __uint_as_float(kCBits);
+  const float x0 = (o[0] + o[1]) * kv, x1 = (o[0] - o[1]) * kv;
+  const float x2 = (o[2] + o[3]) * kv, x3 = (o[2] - o[3]) * kv;
+  o[0] = x0 + x2;
+  o[2] = x0 - x2;
+  o[1] = x1 + x3;
+  o[3] = x1 - x3;
+
+#pragma unroll 4
+  for (int k = 0; k < last; ++k) {
+    const float p = sc[k];
+    if (p > 0.f) {
+      const __nv_bfloat16* v = Vn + k * L.vns.token + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = __fmaf_rn(p, __bfloat162float(v[32 * i]), o[i]);
+    }
+  }
+  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
   __nv_bfloat16* op = static_cast<__nv_bfloat16*>(L.out) + u * L.os.unit + j * L.os.head +
                       node * L.os.token;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) op[lane + 32 * c] = __float2bfloat16_rn(o[c] * inv);
+  for (int i = 0; i < 4; ++i) op[lane + 32 * i] = __float2bfloat16_rn(o[i] * inv);
   if (L.lse && lane == 0)
-    L.lse[(u * L.heads * L.G + j) * L.nodes + node] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    L.lse[(u * L.heads * L.G + j) * L.nodes + node] =
+        sum > 0.f ? (ref + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // ------------------------------------------------------------------ launch
@@ -1017,8 +1159,11 @@ struct TreePlan {
 
 // Rows per CTA: up to 128 columns, blocks of equal width for more rows.
 // Splits: the launch costs (waves of 148 CTAs) * (tiles per CTA + setup, about
-// two tiles); the smallest cost, the fewest splits among equals.
-static TreePlan tree_plan(int units, int heads, int G, int nodes, int64_t n) {
+// three tiles); the smallest cost, the fewest splits among equals.  Units that
+// may hold fewer than n tokens (their lengths are on the device) even out only
+// over CTAs much shorter than the launch: there a CTA takes at most a fourth
+// of an SM's even share, but 12 tiles at least.
+static TreePlan tree_plan(int units, int heads, int G, int nodes, int64_t n, bool ragged) {
   TreePlan p{};
   const int64_t rows = static_cast<int64_t>(nodes) * G;
   p.rblocks = static_cast<int>((rows + 127) / 128);
@@ -1028,16 +1173,22 @@ static TreePlan tree_plan(int units, int heads, int G, int nodes, int64_t n) {
   p.tiles = (n + kTreeTile - 1) / kTreeTile;
   if (p.tiles < 1) p.tiles = 1;
   const int64_t ctas = static_cast<int64_t>(units) * heads * p.rblocks;
+  int64_t most = p.tiles;
+  if (ragged && units > 1) {
+    most = ctas * p.tiles / (148 * 4);
+    most = most < 12 ? 12 : most;
+  }
   int64_t best = -1;
-  for (int64_t s = 1; s <= p.tiles && s <= 4 * 148; ++s) {
+  for (int64_t s = 1; s <= p.tiles && s <= kTreeMaxSplits; ++s) {
     const int64_t per = (p.tiles + s - 1) / s, ns = (p.tiles + per - 1) / per;
-    const int64_t cost = (ctas * ns + 147) / 148 * (per + 2);
+    if (per > most && s < p.tiles && s < kTreeMaxSplits) continue;
+    const int64_t cost = (ctas * ns + 147) / 148 * (per + 3);
     if (best < 0 || cost < best) {
       best = cost;
       p.per = per;
       p.nsplit = ns;
     }
-    if (ctas * s >= 4 * 148 && s > 1) break;  // finer splits only add setup
+    if (best >= 0 && ctas * s >= 8 * 148 && s > 1) break;  // finer splits only add setup
   }
   return p;
 }
@@ -1047,14 +1198,15 @@ static size_t tree_part_bytes(int units, int heads, int G, int nodes, const Tree
   return (b + 255) / 256 * 256;
 }
 
-size_t tree_workspace_bytes(int units, int heads, int G, int nodes, int64_t n, bool shared) {
-  const TreePlan p = tree_plan(units, heads, G, nodes, n);
+size_t tree_workspace_bytes(int units, int heads, int G, int nodes, int64_t n, bool shared,
+                            bool ragged) {
+  const TreePlan p = tree_plan(units, heads, G, nodes, n, ragged);
   return tree_part_bytes(units, heads, G, nodes, p) +
          static_cast<size_t>(shared ? 1 : units) * p.tiles * 16 * 128 * sizeof(uint4);
 }
 
-int64_t tree_ctas(int units, int heads, int G, int nodes, int64_t n) {
-  const TreePlan p = tree_plan(units, heads, G, nodes, n);
+int64_t tree_ctas(int units, int heads, int G, int nodes, int64_t n, bool ragged) {
+  const TreePlan p = tree_plan(units, heads, G, nodes, n, ragged);
   const int64_t a = static_cast<int64_t>(units) * heads * p.rblocks * p.nsplit;
   const int64_t b = static_cast<int64_t>(units) * p.tiles;
   return a > b ? a : b;
@@ -1086,7 +1238,7 @@ cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream) {
   a.rows = L.nodes * L.G;
   a.n_a = (L.rope_max_pos + 255) / 256;
   if (L.n > 0) {
-    const TreePlan p = tree_plan(L.units, L.heads, L.G, L.nodes, L.n);
+    const TreePlan p = tree_plan(L.units, L.heads, L.G, L.nodes, L.n, L.lens != nullptr);
     a.ncols = p.cols;
     a.page = make_fastdiv(static_cast<uint32_t>(L.table ? L.page_size : 1));
     a.rblocks = p.rblocks;
@@ -1098,7 +1250,7 @@ cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream) {
                                         tree_part_bytes(L.units, L.heads, L.G, L.nodes, p));
     a.angle_stride = L.positions ? p.tiles * 16 * 128 : 0;
     const int64_t agrid = p.tiles * (L.positions ? L.units : 1);
-    tree_angles_kernel<<<static_cast<unsigned>(agrid), 512, 0, stream>>>(a);
+    tree_angles_kernel<<<static_cast<unsigned>(agrid), kAngleThreads, 0, stream>>>(a);
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     const int64_t grid = static_cast<int64_t>(L.units) * L.heads * p.rblocks * p.nsplit;
@@ -1110,7 +1262,10 @@ cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream) {
     if (err != cudaSuccess) return err;
   }
   const int64_t rows = static_cast<int64_t>(L.units) * L.heads * a.rows;
-  tree_combine_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
+  const int smem = kCombineWarps * combine_floats(static_cast<int>(a.nsplit), L.nodes) *
+                   static_cast<int>(sizeof(float));  // at most 28 KB
+  tree_combine_kernel<<<static_cast<unsigned>((rows + kCombineWarps - 1) / kCombineWarps),
+                        32 * kCombineWarps, smem, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -108,7 +108,7 @@ def lib() -> ctypes.CDLL:
                                   KVStrides, i32, P]),
         "nq_encode_slots": (i32, [P, KVStrides, P, KVStrides, i32, i64, P, P, i32, i64, P, i64,
                                   PK, PK, P]),
-        "nq_tree_attend_workspace_bytes": (sz, [i32, i32, i32, i32, i64, i32]),
+        "nq_tree_attend_workspace_bytes": (sz, [i32, i32, i32, i32, i64, i32, i32]),
         "nq_tree_attend": (i32, [P, KVStrides, P, KVStrides, P, KVStrides, i32, i32, i32, i32, PK,
                                  PK, i64, P, P, i64, i32, i64, P, i64, i64, P, i64, P, i64,
                                  ctypes.c_float, P, KVStrides, P, P, sz, P]),
@@ -736,8 +736,12 @@ def nq_encode_slots(K: torch.Tensor | None, V: torch.Tensor | None, k_out: Packe
 
 
 def tree_attend_workspace(units: int, heads: int, G: int, nodes: int, n: int,
-                          shared: bool = True, device="cuda") -> torch.Tensor:
-    need = lib().nq_tree_attend_workspace_bytes(units, heads, G, nodes, int(n), int(shared))
+                          shared: bool = True, ragged: bool = False,
+                          device="cuda") -> torch.Tensor:
+    """Workspace of nq_tree_attend: shared without a positions list, ragged
+    with lens."""
+    need = lib().nq_tree_attend_workspace_bytes(units, heads, G, nodes, int(n), int(shared),
+                                                int(ragged))
     return torch.empty(max(need, 16) // 4, dtype=torch.float32, device=device)
 
 
@@ -813,7 +817,8 @@ def nq_tree_attend(q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
             raise ValueError("out must have the shape of q")
         os_ = _strides4(out, bf, "out")
         lse_t = torch.empty(units, Hq, nodes, dtype=torch.float32, device=dev) if lse else None
-        need = L.nq_tree_attend_workspace_bytes(units, heads, G, nodes, n, int(positions is None))
+        need = L.nq_tree_attend_workspace_bytes(units, heads, G, nodes, n, int(positions is None),
+                                                int(lens is not None))
         if ws is None:
             ws = torch.empty(max(need, 16) // 4, dtype=torch.float32, device=dev)
         elif not ws.is_contiguous():

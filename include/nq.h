@@ -486,11 +486,12 @@ nq_status nq_encode_slots(const void *K, nq_kv_strides ks, const void *V, nq_kv_
  * arithmetic's precision, as for any fp32 softmax.
  * 1 <= G <= 8, 0 <= n < 2^31 (n = 0: the draft alone, k_in and v_in are not
  * read), 1 <= nodes <= 1024.  ws: nq_tree_attend_workspace_bytes(units,
- * heads, G, nodes, n, shared) bytes, 16-byte aligned, shared = 1 when
- * positions is NULL (one table of angles for all units), else 0. */
+ * heads, G, nodes, n, shared, ragged) bytes, 16-byte aligned; shared = 1 when
+ * positions is NULL (one table of angles for all units), ragged = 1 when lens
+ * is given, else 0. */
 #define NQ_TREE_MAX_NODES 1024
 size_t nq_tree_attend_workspace_bytes(int units, int heads, int G, int nodes, int64_t n,
-                                      int shared);
+                                      int shared, int ragged);
 nq_status nq_tree_attend(const void *q, nq_kv_strides qs, const void *K_new, nq_kv_strides kns,
                          const void *V_new, nq_kv_strides vns, int units, int heads, int G,
                          int nodes, const nq_packed *k_in, const nq_packed *v_in, int64_t n,

@@ -462,7 +462,7 @@ def check_tree(nq, units, heads, G, nodes, n, bk=3, bv=2, P=0, lens=None, kept=F
         mask = mask[0]
     sc = D ** -0.5 if scale is None else scale
     lt = None if lens is None else i32([x if u % 2 else x for u, x in enumerate(lens)])
-    ws = nq.tree_attend_workspace(units, heads, G, nodes, n, positions is None)
+    ws = nq.tree_attend_workspace(units, heads, G, nodes, n, positions is None, lens is not None)
     ws.fill_(float("nan"))  # nothing of the workspace is read before it is written
     guard = torch.full((units, nodes + 1, heads * G, D), 3.25, dtype=torch.bfloat16, device="cuda")
     buf = guard[:, :nodes].permute(0, 2, 1, 3)
@@ -642,7 +642,7 @@ def test_tree_other_stream_graph_and_repeat(nq):
     side = call(q, stream=s)
     s.synchronize()
     assert torch.equal(side, a)
-    ws = nq.tree_attend_workspace(U, H, G, M, n)
+    ws = nq.tree_attend_workspace(U, H, G, M, n, ragged=True)
     outs, graphs = [torch.empty_like(q), torch.empty_like(q)], []
     for x, o in ((q, outs[0]), (q2, outs[1])):
         gr = torch.cuda.CUDAGraph()

@@ -152,11 +152,11 @@ def test_tree_attend_refusals(nq):
 
 def test_tree_workspace_sizes(nq):
     L = nq.lib()
-    assert L.nq_tree_attend_workspace_bytes(1, 8, 4, 1, 0, 1) == 0
-    assert L.nq_tree_attend_workspace_bytes(0, 8, 4, 1, 100, 1) == 0
-    small = L.nq_tree_attend_workspace_bytes(1, 8, 4, 1, 100, 1)
-    assert 0 < small < L.nq_tree_attend_workspace_bytes(1, 8, 4, 64, 100, 1)
-    assert small <= L.nq_tree_attend_workspace_bytes(1, 8, 4, 1, 100000, 1)
+    assert L.nq_tree_attend_workspace_bytes(1, 8, 4, 1, 0, 1, 0) == 0
+    assert L.nq_tree_attend_workspace_bytes(0, 8, 4, 1, 100, 1, 0) == 0
+    small = L.nq_tree_attend_workspace_bytes(1, 8, 4, 1, 100, 1, 0)
+    assert 0 < small < L.nq_tree_attend_workspace_bytes(1, 8, 4, 64, 100, 1, 0)
+    assert small <= L.nq_tree_attend_workspace_bytes(1, 8, 4, 1, 100000, 1, 0)
 
 
 def test_binding_refuses_host_tensors(nq):

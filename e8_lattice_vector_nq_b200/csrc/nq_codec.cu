@@ -1561,8 +1561,9 @@ static cudaError_t launch_slots(CodecArgs a, cudaStream_t stream) {
   if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
   if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return err;
-  if ((err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, smem)) !=
-      cudaSuccess)
+  // (the query costs more host time than a small call's launch)
+  if (a.num_tiles > sms &&
+      (err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads, smem)) != cudaSuccess)
     return err;
   if (per_sm < 1) per_sm = 1;
   const int64_t grid = min64(a.num_tiles, static_cast<int64_t>(sms) * per_sm);

@@ -176,9 +176,11 @@ __global__ void __launch_bounds__(kPageThreads) page_tables_kernel(const PageTab
 
 cudaError_t launch_page_tables(const PageTablesLaunch& L, cudaStream_t stream) {
   const int smem = (3 * L.requests + 1) * static_cast<int>(sizeof(int32_t));
-  cudaError_t err = cudaFuncSetAttribute(page_tables_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (err != cudaSuccess) return err;
+  if (smem > 48 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(
+        page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+  }
   int64_t grid = (L.max_rows + 4 * kPageThreads - 1) / (4 * kPageThreads);
   const int64_t by_requests = (L.requests + kPageThreads / 32 - 1) / (kPageThreads / 32);
   if (grid < by_requests) grid = by_requests;

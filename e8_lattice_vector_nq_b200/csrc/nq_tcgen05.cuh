@@ -38,16 +38,23 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0u;
 }
 
-// The same with a limit of about ns nanoseconds on that time: a long one keeps
-// a waiting warp from taking issue slots with its polls.
-__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+// Up to `polls` polls in a loop of five instructions: waiting warps share the
+// issue slots of working ones.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint32_t polls) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %3;\n\t"
+      "POLL:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra POLL;\n\t"
+      "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(ns)
+      : "r"(bar), "r"(parity), "r"(polls)
       : "memory");
   return ok != 0u;
 }

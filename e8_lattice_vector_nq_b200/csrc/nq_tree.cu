@@ -55,7 +55,7 @@ constexpr float kTreeStart = 4.0f, kTreeTop = 14.0f;  // log2 of a column's larg
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTreeMaxSplits = 4 * 148;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr uint32_t kTreeWaitLimit = 1u << 16, kTreeWaitNs = 16384;  // about a second
+constexpr uint32_t kTreeWaitLimit = 1u << 12, kTreePolls = 256;  // 2^20 polls
 constexpr uint32_t kErrTreeTimeout = 4u;
 
 struct TreeArgs {
@@ -301,9 +301,9 @@ struct TreeSmem {
 // phase needs something that its waiters do after their wait for this one,
 // and every waiter takes the phases in order.
 __device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
-  bool done = mbar_try_wait_for(bar, parity, kTreeWaitNs);
-  for (uint32_t spin = 1; !done && spin < kTreeWaitLimit; ++spin)
-    done = mbar_try_wait_for(bar, parity, kTreeWaitNs) || *dead;
+  bool done = mbar_poll(bar, parity, kTreePolls);
+  for (uint32_t i = 1; !done && i < kTreeWaitLimit; ++i)
+    done = mbar_poll(bar, parity, kTreePolls) || *dead;
   if (!done) {
     *dead = 1u;
     atomicOr(&g_nq_error, kErrTreeTimeout);

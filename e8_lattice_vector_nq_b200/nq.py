@@ -7,6 +7,7 @@ or the device is not CUDA, the calls fail loudly.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -529,47 +530,46 @@ def nq_entropy_decode(coded: EntropyCoded, out: PackedStore, slot0: int = 0, str
 
 
 # ------------------------------------------------------ serving a paged cache
+# These calls are a server's smallest ones, so the marshalling counts: plain
+# integers go to ctypes as pointers, and every check is one comparison.
 BF16, F32 = 0, 1
 _TYPES = {torch.bfloat16: BF16, torch.float32: F32}
+_NO_CONTEXT = contextlib.nullcontext()
+_NO_STRIDES = KVStrides(0, 0, 0)
 
 
-class _on:
-    """The device and the stream of a call, current while it runs: what the
-    call allocates then belongs to the stream that uses it."""
-
-    def __init__(self, device, stream):
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        if s.device != device:
-            raise ValueError(f"the stream is on {s.device}, the tensors are on {device}")
-        self.ctx = None
-        if torch.cuda.current_device() != device.index or stream is not None:
-            self.ctx = torch.cuda.stream(s)
-        self.ptr = ctypes.c_void_p(s.cuda_stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.ptr
-
-    def __exit__(self, *e):
-        if self.ctx is not None:
-            self.ctx.__exit__(*e)
-
-
-def _same_device(first: torch.Tensor, *ts) -> torch.device:
-    _require_cuda(first, *ts)
+def _device_of(*ts) -> int:
+    """The index of the one CUDA device that holds all the tensors given."""
+    idx = -1
     for t in ts:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-    return first.device
+        if t is not None:
+            d = t.get_device() if t.is_cuda else -1
+            if d < 0:
+                raise ValueError("libnq works on CUDA tensors only (no CPU path)")
+            if d != idx:
+                if idx >= 0:
+                    raise ValueError(f"tensors on different devices: cuda:{idx} and cuda:{d}")
+                idx = d
+    return idx
+
+
+def _stream_on(idx: int, stream):
+    """The stream's handle and the context in which to allocate and launch: the
+    tensors' device, and the given stream, so that what the call allocates
+    belongs to the stream that uses it."""
+    if stream is None:
+        here = torch._C._cuda_getDevice() == idx
+        return torch._C._cuda_getCurrentRawStream(idx), _NO_CONTEXT if here else torch.cuda.device(idx)
+    if stream.device.index != idx:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{idx}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _int32(t: torch.Tensor, shape: tuple, name: str) -> None:
     """An int32 tensor of that shape, its last dimension contiguous."""
-    if t.dtype != torch.int32 or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if t.dtype != torch.int32 or t.shape != shape or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be int32 {list(shape)} with a contiguous last dimension, "
+                         f"got {t.dtype} {list(t.shape)}")
 
 
 def _positions(positions, units: int, n: int) -> int:
@@ -586,8 +586,12 @@ def _strides4(t: torch.Tensor, types, name: str) -> KVStrides:
         raise ValueError(f"{name} must be [units, heads, rows, 128] with a contiguous last "
                          f"dimension, of type {' or '.join(str(x) for x in types)}")
     # a dimension of one index may carry any stride: give it one that is always valid
-    s = [t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
-    return KVStrides(*s)
+    (u, h, r, _), (a, b, c, _) = t.shape, t.stride()
+    return KVStrides(a if u > 1 else 0, b if h > 1 else 0, c if r > 1 else 0)
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
 
 
 @dataclass
@@ -604,8 +608,11 @@ class PageTables:
 
     @classmethod
     def empty(cls, requests: int, max_rows: int, device="cuda") -> "PageTables":
-        e = lambda n: torch.empty(n, dtype=torch.int32, device=device)  # noqa: E731
-        return cls(e(requests), e(requests + 1), e(max_rows), e(max_rows), e(2))
+        pad = -max_rows % 4  # the row lists 16-byte aligned
+        e = torch.empty(2 * (max_rows + pad) + 2 * requests + 3, dtype=torch.int32, device=device)
+        slots, _, pos, _, lens, starts, used = e.split(
+            (max_rows, pad, max_rows, pad, requests, requests + 1, 2))
+        return cls(lens, starts, slots, pos, used)
 
 
 def nq_page_tables(lens: torch.Tensor, counts: torch.Tensor, page_size: int,
@@ -616,29 +623,33 @@ def nq_page_tables(lens: torch.Tensor, counts: torch.Tensor, page_size: int,
     ones (see nq.h, nq_page_tables): fills the fresh entries of table
     [requests][pages per request] in place from free_pages, whose first
     taken[0] pages are gone already (none without taken)."""
-    dev = _same_device(lens, counts, free_pages, table, taken)
+    idx = _device_of(lens, counts, free_pages, table, taken)
     if taken is not None:
         _int32(taken, (1,), "taken")
-    S = lens.shape[0]
+    S, max_rows = lens.shape[0], int(max_rows)
     _int32(lens, (S,), "lens")
     _int32(counts, (S,), "counts")
-    _int32(free_pages, (free_pages.numel(),), "free_pages")
+    _int32(free_pages, (free_pages.shape[0],), "free_pages")
     if table.dim() != 2 or table.shape[0] != S or table.dtype != torch.int32 or not table.is_contiguous():
         raise ValueError(f"table must be a contiguous int32 [{S}, pages] tensor")
-    with _on(dev, stream) as st:
+    if max_rows < 0:
+        raise ValueError("max_rows must be >= 0")
+    st, ctx = _stream_on(idx, stream)
+    with ctx:
         if out is None:
-            out = PageTables.empty(S, int(max_rows), dev)
+            out = PageTables.empty(S, max_rows, lens.device)
         else:
-            _same_device(lens, out.lens, out.starts, out.slots, out.positions, out.used)
+            _device_of(lens, out.lens, out.starts, out.slots, out.positions, out.used)
             _int32(out.lens, (S,), "out.lens")
             _int32(out.starts, (S + 1,), "out.starts")
-            _int32(out.slots, (int(max_rows),), "out.slots")
-            _int32(out.positions, (int(max_rows),), "out.positions")
+            _int32(out.slots, (max_rows,), "out.slots")
+            _int32(out.positions, (max_rows,), "out.positions")
             _int32(out.used, (2,), "out.used")
-        _check(lib().nq_page_tables(_ptr(lens), _ptr(counts), S, int(page_size), _ptr(free_pages),
-                                    free_pages.numel(), _ptr(taken), _ptr(table), max(table.shape[1], 1),
-                                    _ptr(out.lens), _ptr(out.starts), _ptr(out.slots),
-                                    _ptr(out.positions), int(max_rows), _ptr(out.used), st))
+        _check(lib().nq_page_tables(lens.data_ptr(), counts.data_ptr(), S, page_size,
+                                    free_pages.data_ptr(), free_pages.shape[0], _addr(taken),
+                                    table.data_ptr(), max(table.shape[1], 1), out.lens.data_ptr(),
+                                    out.starts.data_ptr(), out.slots.data_ptr(),
+                                    out.positions.data_ptr(), max_rows, out.used.data_ptr(), st))
     return out
 
 
@@ -656,37 +667,42 @@ def nq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope_tab: to
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q and k are both None")
-    dev = _same_device(ref, q, k, rope_tab, positions, q_weight, k_weight, q_out, k_out)
-    units, rows = ref.shape[0], ref.shape[2]
-    types = tuple(_TYPES)
-    for t, w, name in ((q, q_weight, "q"), (k, k_weight, "k")):
-        if t is not None and (t.dim() != 4 or t.shape[0] != units or t.shape[2] != rows
-                              or t.dtype != ref.dtype):
-            raise ValueError("q and k must share units, rows and type")
-        if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (D,) or w.stride(0) != 1):
-            raise ValueError(f"{name}_weight must be float32 [128]")
+    idx = _device_of(ref, q, k, rope_tab, positions, q_weight, k_weight, q_out, k_out)
+    if ref.dim() != 4 or (q is not None and k is not None and
+                          (q.dim() != 4 or k.dim() != 4 or q.shape[0] != k.shape[0]
+                           or q.shape[2] != k.shape[2] or q.dtype != k.dtype)):
+        raise ValueError("q and k must be [units, heads, rows, 128] of the same units, rows and type")
+    units, _, rows, _ = ref.shape
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != torch.float32 or w.shape != (D,) or w.stride(0) != 1):
+            raise ValueError("weights must be float32 [128]")
     ps = _positions(positions, units, rows) if positions is not None else 0
-    with _on(dev, stream) as st:
-        args, outs = [], []
-        for t, o, dt, name in ((q, q_out, q_dtype, "q"), (k, k_out, k_dtype, "k")):
-            if t is None:
-                args.append((None, KVStrides(0, 0, 0), 0, None, KVStrides(0, 0, 0), BF16))
-                outs.append(None)
-                continue
-            s = _strides4(t, types, name)
-            if o is None:
-                o = torch.empty(t.shape, dtype=dt or t.dtype, device=dev)
-            elif tuple(o.shape) != tuple(t.shape) or (dt is not None and dt != o.dtype):
-                raise ValueError(f"{name}_out must have the shape of {name} and the type asked for")
-            os_ = _strides4(o, types, name + "_out")
-            args.append((_ptr(t), s, t.shape[1], _ptr(o), os_, _TYPES[o.dtype]))
-            outs.append(o)
-        (qp, qs, hq, qo, qos, qt), (kp, ks, hk, ko, kos, kt) = args
-        _check(lib().nq_qk_norm_rope(qp, qs, hq, kp, ks, hk, _TYPES[ref.dtype], units, rows,
-                                     _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions),
-                                     ps, int(pos_base), _ptr(rope_tab), int(rope_max_pos), qo, qos,
-                                     qt, ko, kos, kt, st))
-    return outs[0], outs[1]
+    st, ctx = _stream_on(idx, stream)
+    with ctx:
+        qs = ks = qos = kos = _NO_STRIDES
+        qt = kt = hq = hk = 0
+        if q is not None:
+            qs, hq = _strides4(q, _TYPES, "q"), q.shape[1]
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q_dtype or q.dtype, device=q.device)
+            elif q_out.shape != q.shape or (q_dtype is not None and q_dtype != q_out.dtype):
+                raise ValueError("q_out must have the shape of q and the type asked for")
+            qos = _strides4(q_out, _TYPES, "q_out")
+            qt = _TYPES[q_out.dtype]
+        if k is not None:
+            ks, hk = _strides4(k, _TYPES, "k"), k.shape[1]
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=k_dtype or k.dtype, device=k.device)
+            elif k_out.shape != k.shape or (k_dtype is not None and k_dtype != k_out.dtype):
+                raise ValueError("k_out must have the shape of k and the type asked for")
+            kos = _strides4(k_out, _TYPES, "k_out")
+            kt = _TYPES[k_out.dtype]
+        _check(lib().nq_qk_norm_rope(_addr(q), qs, hq, _addr(k), ks, hk, _TYPES[ref.dtype], units,
+                                     rows, _addr(q_weight), _addr(k_weight), eps, _addr(positions),
+                                     ps, pos_base, rope_tab.data_ptr(), rope_max_pos,
+                                     _addr(q_out) if hq else None, qos, qt,
+                                     _addr(k_out) if hk else None, kos, kt, st))
+    return (q_out if q is not None else None), (k_out if k is not None else None)
 
 
 def nq_encode_slots(K: torch.Tensor | None, V: torch.Tensor | None, k_out: PackedStore | None,
@@ -700,39 +716,37 @@ def nq_encode_slots(K: torch.Tensor | None, V: torch.Tensor | None, k_out: Packe
     if ref is None:
         raise ValueError("K and V are both None")
     _require_device_readable(K, V)
-    stores = [s for t, s in ((K, k_out), (V, v_out)) if t is not None]
-    if any(s is None for s in stores):
-        raise ValueError("K needs k_out and V needs v_out")
-    dev = _same_device(slots, positions, rope_tab, *(t for s in stores for t in (s.codes, s.meta)),
-                       *(t for t in (K, V) if t is not None and t.is_cuda))
+    idx = _device_of(slots, positions, rope_tab, *(t for t in (K, V) if t is not None and t.is_cuda))
     if ref.dim() != 3:
         raise ValueError("K and V must be [heads, rows, 128]")
-    heads, rows = ref.shape[0], ref.shape[1]
+    heads, rows, _ = ref.shape
     _int32(slots, (rows,), "slots")
     if K is not None and positions is None:
         raise ValueError("keys need positions")
     if positions is not None:
         _int32(positions, (rows,), "positions")
-    pages, _, P = stores[0].meta.shape
-    for s in stores:
-        if tuple(s.meta.shape) != (pages, heads, P):
-            raise ValueError("the stores must be [pages][heads][page_size] alike")
-    view = lambda t: t[None] if t is not None else None  # noqa: E731
-    for t in (K, V):
-        if t is not None and tuple(t.shape) != (heads, rows, D):
-            raise ValueError("K and V must be [heads, rows, 128] alike")
+    shape, desc, strides = None, [], []
+    for t, s in ((K, k_out), (V, v_out)):
+        if t is None:
+            desc.append(None)
+            strides.append(_NO_STRIDES)
+            continue
+        if s is None:
+            raise ValueError("K needs k_out and V needs v_out")
+        if t.shape != (heads, rows, D) or t.dtype != torch.bfloat16 or t.stride(2) != 1:
+            raise ValueError("K and V must be bf16 [heads, rows, 128] alike, the last dimension contiguous")
+        shape = shape or s.meta.shape
+        if s.meta.shape != shape or shape[1] != heads or s.meta.get_device() != idx:
+            raise ValueError("the stores must be [pages][heads][page_size] alike, on the tensors' device")
+        desc.append(ctypes.byref(s.desc()))
+        strides.append(KVStrides(0, t.stride(0) if heads > 1 else 0, t.stride(1) if rows > 1 else 0))
     if rows == 0:  # an empty tensor has no address
         return
-    none = KVStrides(0, 0, 0)
-    kd = k_out.desc() if K is not None else None
-    vd = v_out.desc() if V is not None else None
-    with _on(dev, stream) as st:
-        _check(lib().nq_encode_slots(
-            _ptr(K), _strides4(view(K), (torch.bfloat16,), "K") if K is not None else none,
-            _ptr(V), _strides4(view(V), (torch.bfloat16,), "V") if V is not None else none,
-            heads, rows, _ptr(slots), _ptr(positions), P, pages, _ptr(rope_tab),
-            int(rope_max_pos), ctypes.byref(kd) if kd is not None else None,
-            ctypes.byref(vd) if vd is not None else None, st))
+    st, ctx = _stream_on(idx, stream)
+    with ctx:
+        _check(lib().nq_encode_slots(_addr(K), strides[0], _addr(V), strides[1], heads, rows,
+                                     slots.data_ptr(), _addr(positions), shape[2], shape[0],
+                                     _addr(rope_tab), rope_max_pos, desc[0], desc[1], st))
 
 
 def tree_attend_workspace(units: int, heads: int, G: int, nodes: int, n: int,
@@ -762,75 +776,77 @@ def nq_tree_attend(q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
     tokens held (None: n for every unit).  table: int32 [units][pages per
     unit], then k_in and v_in are [pages][heads][page_size].  Returns out like
     q (bf16), or (out, lse fp32 [units][heads*G][nodes]) with lse=True."""
-    dev = _same_device(q, K_new, V_new, rope_tab, mask, lens, table, positions, out, ws,
-                       *(t for s in (k_in, v_in) if s is not None for t in (s.codes, s.meta)))
+    idx = _device_of(q, K_new, V_new, rope_tab, mask, lens, table, positions, out, ws)
     bf = (torch.bfloat16,)
     qs, kns, vns = _strides4(q, bf, "q"), _strides4(K_new, bf, "K_new"), _strides4(V_new, bf, "V_new")
     units, Hq, nodes, _ = q.shape
-    heads = K_new.shape[1]
+    heads, n = K_new.shape[1], int(n)
     if heads < 1 or Hq % heads:
         raise ValueError("q has %d heads, not a multiple of the %d KV heads" % (Hq, heads))
-    if tuple(K_new.shape) != (units, heads, nodes, D) or tuple(V_new.shape) != tuple(K_new.shape):
+    if K_new.shape != (units, heads, nodes, D) or V_new.shape != K_new.shape:
         raise ValueError("K_new and V_new must be [units, heads, nodes, 128]")
-    G, n = Hq // heads, int(n)
+    G = Hq // heads
     page, pages, tstride, ps, ms = 1, 0, 0, 0, 0
     kd = vd = None
     if n > 0:
         if k_in is None or v_in is None or rope_tab is None:
             raise ValueError("n > 0 needs k_in, v_in and rope_tab")
         lead, h, cap = k_in.meta.shape
-        if tuple(v_in.meta.shape) != (lead, h, cap) or h != heads:
+        if v_in.meta.shape != (lead, h, cap) or h != heads:
             raise ValueError("k_in and v_in must be [units or pages][heads][slots] alike")
+        if k_in.meta.get_device() != idx or v_in.meta.get_device() != idx:
+            raise ValueError("the stores must be on the queries' device")
         if table is None:
             if lead < units or cap < n:
                 raise ValueError("packed store too small for units x n")
         else:
             if table.dim() != 2 or table.shape[0] != units or table.dtype != torch.int32:
                 raise ValueError(f"table must be int32 [{units}, pages]")
-            if table.shape[1] > 1 and table.stride(1) != 1:
+            width = table.shape[1]
+            if width > 1 and table.stride(1) != 1:
                 raise ValueError("table must be contiguous in its last dimension")
             page, pages = cap, lead
-            if table.shape[1] * page < n:
+            if width * page < n:
                 raise ValueError("a table row holds fewer than n tokens")
-            tstride = table.stride(0) if units > 1 else table.shape[1]
-            if units > 1 and tstride < table.shape[1]:
+            tstride = table.stride(0) if units > 1 else width
+            if tstride < width:
                 raise ValueError("table rows overlap")
         if positions is not None:
             ps = _positions(positions, units, n)
             if units > 1 and ps < n:
                 raise ValueError("positions rows overlap")
-        kd, vd = k_in.desc(), v_in.desc()
+        kd, vd = ctypes.byref(k_in.desc()), ctypes.byref(v_in.desc())
+    else:
+        table = positions = None
     if lens is not None:
         _int32(lens, (units,), "lens")
     if mask is not None:
         words = (nodes + 63) // 64
-        if mask.dtype != torch.int64 or tuple(mask.shape) not in ((units, nodes, words), (nodes, words)):
+        if mask.dtype != torch.int64 or mask.shape not in ((units, nodes, words), (nodes, words)):
             raise ValueError(f"mask must be int64 [{units}, {nodes}, {words}] or [{nodes}, {words}]")
-        if not (mask if mask.dim() == 2 else mask[0] if units else mask).is_contiguous():
+        if (mask.stride(-1) != 1 and words > 1) or (mask.stride(-2) != words and nodes > 1):
             raise ValueError("mask rows must be contiguous")
         ms = mask.stride(0) if mask.dim() == 3 and units > 1 else 0
     L = lib()
-    with _on(dev, stream) as st:
+    st, ctx = _stream_on(idx, stream)
+    with ctx:
         if out is None:
-            out = torch.empty(units, Hq, nodes, D, dtype=torch.bfloat16, device=dev)
-        elif tuple(out.shape) != tuple(q.shape):
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        elif out.shape != q.shape:
             raise ValueError("out must have the shape of q")
-        os_ = _strides4(out, bf, "out")
-        lse_t = torch.empty(units, Hq, nodes, dtype=torch.float32, device=dev) if lse else None
-        need = L.nq_tree_attend_workspace_bytes(units, heads, G, nodes, n, int(positions is None),
-                                                int(lens is not None))
+        lse_t = torch.empty(units, Hq, nodes, dtype=torch.float32, device=q.device) if lse else None
         if ws is None:
-            ws = torch.empty(max(need, 16) // 4, dtype=torch.float32, device=dev)
+            need = L.nq_tree_attend_workspace_bytes(units, heads, G, nodes, n, positions is None,
+                                                    lens is not None)
+            ws = torch.empty(need // 4 + 4, dtype=torch.float32, device=q.device)
         elif not ws.is_contiguous():
             raise ValueError("ws must be contiguous")
         _check(L.nq_tree_attend(
-            _ptr(q), qs, _ptr(K_new), kns, _ptr(V_new), vns, units, heads, G, nodes,
-            ctypes.byref(kd) if kd is not None else None,
-            ctypes.byref(vd) if vd is not None else None, n, _ptr(lens),
-            _ptr(table) if n > 0 else None, tstride, page, pages,
-            _ptr(positions) if n > 0 else None, ps, int(pos_base), _ptr(rope_tab),
-            int(rope_max_pos), _ptr(mask), ms, float(scale if scale is not None else D ** -0.5),
-            _ptr(out), os_, _ptr(lse_t), _ptr(ws), ws.numel() * ws.element_size(), st))
+            q.data_ptr(), qs, K_new.data_ptr(), kns, V_new.data_ptr(), vns, units, heads, G, nodes,
+            kd, vd, n, _addr(lens), _addr(table), tstride, page, pages, _addr(positions), ps,
+            pos_base, _addr(rope_tab), rope_max_pos, _addr(mask), ms,
+            D ** -0.5 if scale is None else scale, out.data_ptr(), _strides4(out, bf, "out"),
+            _addr(lse_t), ws.data_ptr(), ws.numel() * ws.element_size(), st))
     return (out, lse_t) if lse else out
 
 

@@ -196,7 +196,8 @@ cudaError_t launch_page_tables(const PageTablesLaunch& L, cudaStream_t stream) {
 // coordinates 8l..8l+7 and their RoPE partners 64+8l..64+8l+7, so the rotation
 // stays in the lane, the sum of squares takes three shuffles, and each half
 // row is one 128-byte run of 16-byte accesses.  A group keeps its token's
-// (cos, sin) in registers for several heads, four heads' loads in flight.
+// (cos, sin) in registers for several heads and always has the next heads'
+// loads in flight: what bounds a long call is the bytes under way.
 constexpr int kNormThreads = 256;
 
 struct NormArgs {
@@ -206,26 +207,36 @@ struct NormArgs {
   int chunks;          // items per token
 };
 
+// A lane's share of a row as it is in memory: coordinates 8l .. 8l+7, then
+// their partners.
 template <bool F32>
-__device__ __forceinline__ void norm_load(const void* p, int64_t off, int l, float (&x)[16]) {
-  if (F32) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + off);
+struct NormRaw {
+  uint4 v[F32 ? 4 : 2];
+};
+
+template <bool F32>
+__device__ __forceinline__ void norm_load(const void* p, int64_t off, int l, NormRaw<F32>& r) {
+  if constexpr (F32) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + off);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float4 v = __ldcs(s + (c < 2 ? 2 * l + c : 16 + 2 * l + c - 2));
-      x[4 * c] = v.x;
-      x[4 * c + 1] = v.y;
-      x[4 * c + 2] = v.z;
-      x[4 * c + 3] = v.w;
-    }
+    for (int c = 0; c < 4; ++c) r.v[c] = __ldcs(s + (c < 2 ? 2 * l + c : 16 + 2 * l + c - 2));
   } else {
     const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + off);
+    r.v[0] = __ldcs(s + l);
+    r.v[1] = __ldcs(s + l + 8);
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void norm_floats(const NormRaw<F32>& r, float (&x)[16]) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint4 v = __ldcs(s + l + 8 * c);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int c = 0; c < (F32 ? 4 : 2); ++c) {
+    const uint32_t w[4] = {r.v[c].x, r.v[c].y, r.v[c].z, r.v[c].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F32) {
+        x[4 * c + i] = __uint_as_float(w[i]);
+      } else {
         x[8 * c + 2 * i] = bf16lo(w[i]);
         x[8 * c + 2 * i + 1] = bf16hi(w[i]);
       }
@@ -256,14 +267,16 @@ __device__ __forceinline__ void norm_store(void* p, int64_t off, int l, bool f32
   }
 }
 
-__device__ __forceinline__ void load_weight(const float* w, int l, float (&g)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) g[i] = w ? __ldg(w + (i < 8 ? 8 * l + i : 56 + 8 * l + i)) : 1.0f;
-}
-
 template <bool F32>
-__global__ void __launch_bounds__(kNormThreads, 3) norm_rope_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, 2) norm_rope_kernel(const NormArgs a) {
+  __shared__ __align__(16) float weights[2][kD];  // of the queries, of the keys
   const NormRopeLaunch& L = a.L;
+  {
+    const int i = threadIdx.x & 127;
+    const float* w = threadIdx.x < 128 ? L.q_weight : L.k_weight;
+    weights[threadIdx.x >> 7][i] = w ? __ldg(w + i) : 1.0f;
+  }
+  __syncthreads();
   const int l = threadIdx.x & 7;
   const int64_t item = (static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x) >> 3;
   if (item >= a.items) return;  // a whole group
@@ -287,40 +300,53 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rope_kernel(const NormAr
   }
   const int heads = L.q_heads + L.k_heads;
   const int h0 = chunk * a.per, h1 = min(h0 + a.per, heads);
-  float g[16];
-  load_weight(h0 < L.q_heads ? L.q_weight : L.k_weight, l, g);
   // the groups of a warp may run different numbers of heads: each shuffles alone
   const uint32_t lanes = 0xFFu << (threadIdx.x & 24);
-  constexpr int kU = 2;  // heads whose loads are in flight together
-  for (int h = h0; h < h1; h += kU) {
-    float x[kU][16];
+  constexpr int kU = F32 ? 1 : 2;  // heads per step; those of the next step are in flight
+  NormRaw<F32> next[kU];
+  auto fetch = [&](int h) {
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int hh = min(h + i, h1 - 1);
       if (hh < L.q_heads)
-        norm_load<F32>(L.q, u * L.qs.unit + hh * L.qs.head + t * L.qs.token, l, x[i]);
+        norm_load<F32>(L.q, u * L.qs.unit + hh * L.qs.head + t * L.qs.token, l, next[i]);
       else
-        norm_load<F32>(L.k, u * L.ks.unit + (hh - L.q_heads) * L.ks.head + t * L.ks.token, l, x[i]);
+        norm_load<F32>(L.k, u * L.ks.unit + (hh - L.q_heads) * L.ks.head + t * L.ks.token, l, next[i]);
     }
+  };
+  fetch(h0);
+  for (int h = h0; h < h1; h += kU) {
+    NormRaw<F32> cur[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) cur[i] = next[i];
+    if (h + kU < h1) fetch(h + kU);
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const int hh = h + i;
       if (hh >= h1) break;
-      if (hh == L.q_heads && hh > h0) load_weight(L.k_weight, l, g);
+      const bool is_q = hh < L.q_heads;
+      float x[16], o[16];
+      norm_floats<F32>(cur[i], x);
       float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) ss = __fmaf_rn(x[i][e], x[i][e], ss);
+      for (int e = 0; e < 16; ++e) ss = __fmaf_rn(x[e], x[e], ss);
 #pragma unroll
-      for (int o = 4; o >= 1; o >>= 1) ss += __shfl_xor_sync(lanes, ss, o);
+      for (int o2 = 4; o2 >= 1; o2 >>= 1) ss += __shfl_xor_sync(lanes, ss, o2);
       const float r = __frsqrt_rn(__fmaf_rn(ss, 1.0f / 128.0f, L.eps));
-      float o[16];
+      const float4* g = reinterpret_cast<const float4*>(weights[is_q ? 0 : 1]) + 2 * l;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y0 = x[i][e] * r * g[e], y1 = x[i][e + 8] * r * g[e + 8];
-        o[e] = __fmaf_rn(y0, c[e], -__fmul_rn(y1, s[e]));
-        o[e + 8] = __fmaf_rn(y1, c[e], __fmul_rn(y0, s[e]));
+      for (int e4 = 0; e4 < 2; ++e4) {
+        const float4 ga = g[e4], gb = g[16 + e4];
+        const float wa[4] = {ga.x, ga.y, ga.z, ga.w}, wb[4] = {gb.x, gb.y, gb.z, gb.w};
+#pragma unroll
+        for (int e2 = 0; e2 < 4; ++e2) {
+          const int e = 4 * e4 + e2;
+          const float y0 = x[e] * r * wa[e2], y1 = x[e + 8] * r * wb[e2];
+          o[e] = __fmaf_rn(y0, c[e], -__fmul_rn(y1, s[e]));
+          o[e + 8] = __fmaf_rn(y1, c[e], __fmul_rn(y0, s[e]));
+        }
       }
-      if (hh < L.q_heads)
+      if (is_q)
         norm_store(L.q_out, u * L.qos.unit + hh * L.qos.head + t * L.qos.token, l, L.q_f32, o);
       else
         norm_store(L.k_out, u * L.kos.unit + (hh - L.q_heads) * L.kos.head + t * L.kos.token, l,
@@ -335,10 +361,10 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& L, cudaStream_t stream) {
   a.n_a = (L.rope_max_pos + 255) / 256;
   const int heads = L.q_heads + L.k_heads;
   const int64_t tokens = static_cast<int64_t>(L.units) * L.rows;
-  // Heads per group: enough groups to fill the GPU first (148 SMs x 48 warps
-  // x 4 groups), then up to eight heads share one token's angles.
-  int64_t per = tokens * heads / (148 * 48 * 4);
-  per = per < 1 ? 1 : (per > 8 ? 8 : per);
+  // Heads per group: enough groups to fill the GPU first (148 SMs x 16 warps
+  // x 4 groups, twice over), then up to sixteen heads share one token's angles.
+  int64_t per = tokens * heads / (148 * 16 * 4 * 2);
+  per = per < 1 ? 1 : (per > 16 ? 16 : per);
   a.per = static_cast<int>(per > heads ? heads : per);
   a.chunks = (heads + a.per - 1) / a.per;
   a.items = tokens * a.chunks;

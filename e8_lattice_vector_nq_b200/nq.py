@@ -608,10 +608,9 @@ class PageTables:
 
     @classmethod
     def empty(cls, requests: int, max_rows: int, device="cuda") -> "PageTables":
-        pad = -max_rows % 4  # the row lists 16-byte aligned
-        e = torch.empty(2 * (max_rows + pad) + 2 * requests + 3, dtype=torch.int32, device=device)
-        slots, _, pos, _, lens, starts, used = e.split(
-            (max_rows, pad, max_rows, pad, requests, requests + 1, 2))
+        e = torch.empty(2 * max_rows + 2 * requests + 3, dtype=torch.int32, device=device)
+        slots, pos, lens, starts, used = e.split(
+            (max_rows, max_rows, requests, requests + 1, 2))
         return cls(lens, starts, slots, pos, used)
 
 

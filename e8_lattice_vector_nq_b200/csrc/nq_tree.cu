@@ -104,24 +104,33 @@ __global__ void __launch_bounds__(kAngleThreads) tree_angles_kernel(const TreeAr
   }
   const float4* tab = reinterpret_cast<const float4*>(a.L.rope_tab);
   const int pos32 = static_cast<int>(mine);  // below 2^31: the ABI layer checks
-  // nearby positions share the coarse row: it is read again only when it changes
+  // eight fine rows in flight; nearby positions share the coarse row, which is
+  // read again only when it changes
   int64_t row = -1;
   float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = 0; i < kPer; ++i) {
-    const int pos = __shfl_sync(0xffffffffu, pos32, i);
-    const float4 B = __ldg(tab + (a.n_a + (pos & 255)) * 32 + lane);
-    const int64_t hi = min64(pos >> 8, a.n_a - 1);
-    if (hi != row) A = __ldg(tab + hi * 32 + lane);
-    row = hi;
-    const float c0 = __fmaf_rn(A.x, B.x, -__fmul_rn(A.y, B.y));
-    const float s0 = __fmaf_rn(A.y, B.x, __fmul_rn(A.x, B.y));
-    const float c1 = __fmaf_rn(A.z, B.z, -__fmul_rn(A.w, B.w));
-    const float s1 = __fmaf_rn(A.w, B.z, __fmul_rn(A.z, B.w));
-    const __half2 cc = __floats2half2_rn(c0 - s0, c1 - s1);
-    const __half2 ss = __floats2half2_rn(c0 + s0, c1 + s1);
-    *reinterpret_cast<uint2*>(rows + (first + i) * kAnglePitch + lane * 8) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&cc), *reinterpret_cast<const uint32_t*>(&ss));
+#pragma unroll
+  for (int i0 = 0; i0 < kPer; i0 += 8) {
+    float4 B[8];
+    int pos[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      pos[i] = __shfl_sync(0xffffffffu, pos32, i0 + i);
+      B[i] = __ldg(tab + (a.n_a + (pos[i] & 255)) * 32 + lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t hi = min64(pos[i] >> 8, a.n_a - 1);
+      if (hi != row) A = __ldg(tab + hi * 32 + lane);
+      row = hi;
+      const float c0 = __fmaf_rn(A.x, B[i].x, -__fmul_rn(A.y, B[i].y));
+      const float s0 = __fmaf_rn(A.y, B[i].x, __fmul_rn(A.x, B[i].y));
+      const float c1 = __fmaf_rn(A.z, B[i].z, -__fmul_rn(A.w, B[i].w));
+      const float s1 = __fmaf_rn(A.w, B[i].z, __fmul_rn(A.z, B[i].w));
+      const __half2 cc = __floats2half2_rn(c0 - s0, c1 - s1);
+      const __half2 ss = __floats2half2_rn(c0 + s0, c1 + s1);
+      *reinterpret_cast<uint2*>(rows + (first + i0 + i) * kAnglePitch + lane * 8) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&cc), *reinterpret_cast<const uint32_t*>(&ss));
+    }
   }
   __syncthreads();
   uint4* out = a.angles + u * a.angle_stride + tile * (16 * kTreeTile);
@@ -283,8 +292,8 @@ struct TreeSmem {
   static constexpr int Vm = Kap + 8 * 512;              // value scale mantissas of 8 tiles
   static constexpr int FM = Vm + 8 * 512;               // (f0, f1, -m0, -m1) per row pair
   static constexpr int WMax = FM + N * 8;               // [N][4 warps]
-  static constexpr int WOr = WMax + N * 16;             // [2][4 warps]
-  static constexpr int Bars = WOr + 32;
+  static constexpr int WOr = WMax + N * 16;             // [4][4 warps]
+  static constexpr int Bars = WOr + 64;
   static constexpr int Bytes = Bars + 128 + 1024;       // 1 KB of slack to align the base
   static_assert(Bytes <= 232448, "one CTA per SM within 227 KB");
   // TMEM columns (all 512 are allocated): X (one or two tiles), S, O, and the
@@ -333,20 +342,19 @@ template <int REGS>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
-// Warpgroups of the roles (KW: threads that share a token's key) and their
-// registers per thread, out of Launch x threads that the block starts with.
-// Up to 64 columns the key warpgroups bound the pipeline, so they are four;
-// with 128 the softmax does, and it needs the registers.
+// Warpgroups of the roles (KW: threads that share a token's key, SW: that
+// share its scores) and their registers per thread, out of Launch x threads
+// that the block starts with.  Up to 64 columns the key warpgroups bound the
+// pipeline, so they are four; with 128 the softmax would, and gets four.
 template <int N>
 struct TreeRoles {
-  static constexpr int KW = N > 64 ? 2 : 4;
-  static constexpr int Values0 = 4 * KW, Softmax0 = Values0 + 4, Issue0 = Softmax0 + 8;  // warps
-  static constexpr int Threads = 32 * (Issue0 + 4);
-  static constexpr int Launch = N > 64 ? 80 : 64;
-  static constexpr int Softmax = N > 64 ? 128 : (N > 32 ? 96 : 64), Keys = N > 64 ? 64 : (N > 32 ? 56 : 64),
-                       Values = N > 64 ? 56 : (N > 32 ? 56 : 64), Issue = N > 64 ? 40 : (N > 32 ? 32 : 64);
-  static_assert(2 * Softmax + KW * Keys + Values + Issue <= Threads / 128 * Launch,
-                "the launch's registers");
+  static constexpr int KW = N > 64 ? 2 : 4, SW = N > 64 ? 4 : 2;
+  static constexpr int Values0 = 4 * KW, Softmax0 = Values0 + 4, Issue0 = Softmax0 + 4 * SW;  // warps
+  static constexpr int Threads = 32 * (Issue0 + 4), Launch = 64;
+  static_assert(Threads == 1024, "eight warpgroups");
+  static constexpr int Softmax = N > 64 ? 88 : (N > 32 ? 96 : 64), Keys = N > 64 ? 48 : (N > 32 ? 56 : 64),
+                       Values = N > 64 ? 40 : (N > 32 ? 56 : 64), Issue = N > 64 ? 24 : (N > 32 ? 32 : 64);
+  static_assert(SW * Softmax + KW * Keys + Values + Issue <= 8 * Launch, "the launch's registers");
 };
 template <int LAUNCH, int WANT>
 __device__ __forceinline__ void set_regs() {
@@ -453,12 +461,12 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
     mbar_init(bar_t, 4 * KW);
     mbar_init(bar_x, 1);
     mbar_init(bar_xf, 4 * KW);
-    mbar_init(bar_sf, 8);
+    mbar_init(bar_sf, 4 * R::SW);
     for (int j = 0; j < 2; ++j) {
       mbar_init(bar_k(j), 4 * KW);
       mbar_init(bar_s(j), 2);  // the products, and their issuer (see there)
       mbar_init(bar_v(j), 4);
-      mbar_init(bar_p(j), 8);
+      mbar_init(bar_p(j), 4 * R::SW);
       mbar_init(bar_o(j), 1);
     }
     *dead = 0u;
@@ -572,7 +580,8 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
         }
       }
       meta = __ldg(L.k_in.meta + v);
-      vmeta = __ldg(L.v_in.meta + (held ? lead * L.v_in.unit_stride + vhead + slot : 0));
+      if (kw == KW - 1)
+        vmeta = __ldg(L.v_in.meta + (held ? lead * L.v_in.unit_stride + vhead + slot : 0));
     };
     // codes of tile j -> T; then the loads of tile j+1
     auto write_t = [&](int j) {
@@ -729,7 +738,7 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
     // Thread (t, w): token t, query rows HN w .. HN w + HN - 1 of the block.
     setup_done();
     set_regs<R::Launch, R::Softmax>();
-    constexpr int HN = N / 2, CH = HN < 32 ? HN : 32;  // columns; columns at a time
+    constexpr int HN = N / R::SW, CH = HN < 32 ? HN : 32;  // columns; columns at a time
     const int w = (warp - R::Softmax0) >> 2, wl = warp & 3;
     const uint32_t bid = 1 + w;  // this warpgroup's named barrier
     float4* fm = reinterpret_cast<float4*>(gen + S::FM) + w * (HN / 2);
@@ -1017,10 +1026,10 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Shared floats of a warp: split factors, draft scores (then weights, 0: not
-// seen), the query.
+// Shared words of a warp: split factors, the draft nodes seen, their scores
+// (then weights), the query.
 __host__ __device__ constexpr int combine_floats(int nsplit, int nodes) {
-  return (nsplit + nodes + 3) / 4 * 4 + kD;  // the query 16-byte aligned
+  return (nsplit + 2 * nodes + 3) / 4 * 4 + kD;  // the query 16-byte aligned
 }
 
 __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const TreeArgs a) {
@@ -1032,6 +1041,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   const int ns = static_cast<int>(a.nsplit);
   float* fac = combine_smem + (threadIdx.x >> 5) * combine_floats(ns, L.nodes);
   float* sc = fac + ns;
+  int* list = reinterpret_cast<int*>(sc + L.nodes);
   float* qs = fac + combine_floats(ns, L.nodes) - kD;
   const int r = static_cast<int>(w % a.rows);
   const int64_t uh = w / a.rows, u = uh / L.heads;
@@ -1050,22 +1060,33 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   }
   __syncwarp();
 
-  // draft scores, four nodes at a time
+  // the nodes that the row sees, in order
   const int words = (L.nodes + 63) / 64;
-  const unsigned long long* mask =
-      L.mask ? reinterpret_cast<const unsigned long long*>(L.mask) + u * L.mask_stride +
-                   static_cast<int64_t>(node) * words
-             : nullptr;
-  const int last = mask ? L.nodes : node + 1;  // a chain sees nodes 0 .. node
+  int seen = 0;
+  if (!L.mask) {  // a chain sees nodes 0 .. node
+    seen = node + 1;
+    for (int k = lane; k < seen; k += 32) list[k] = k;
+  } else {
+    const uint32_t* mask = reinterpret_cast<const uint32_t*>(
+        L.mask + u * L.mask_stride + static_cast<int64_t>(node) * words);
+    for (int k0 = 0; k0 < L.nodes; k0 += 32) {
+      uint32_t bits = __ldg(mask + (k0 >> 5));
+      if (L.nodes - k0 < 32) bits &= (1u << (L.nodes - k0)) - 1u;
+      if (bits >> lane & 1u) list[seen + __popc(bits & ((1u << lane) - 1u))] = k0 + lane;
+      seen += __popc(bits);
+    }
+  }
+  __syncwarp();
+
+  // their scores, four nodes at a time
   const __nv_bfloat16* Kn = static_cast<const __nv_bfloat16*>(L.K_new) + u * L.kns.unit + h * L.kns.head;
   const __nv_bfloat16* Vn = static_cast<const __nv_bfloat16*>(L.V_new) + u * L.vns.unit + h * L.vns.head;
 #pragma unroll 2
-  for (int k0 = 0; k0 < last; k0 += 4) {
+  for (int k0 = 0; k0 < seen; k0 += 4) {
     const int k = k0 + (lane >> 3), e = lane & 7;  // lane e: coordinates 8e .. +7, 64 + 8e .. +7
-    const bool seen = k < last && (!mask || (__ldg(mask + (k >> 6)) >> (k & 63) & 1ull));
     float s = 0.f;
-    if (seen) {
-      const uint4* src = reinterpret_cast<const uint4*>(Kn + k * L.kns.token);
+    if (k < seen) {
+      const uint4* src = reinterpret_cast<const uint4*>(Kn + list[k] * L.kns.token);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const uint4 v = __ldg(src + 8 * hf + e);
@@ -1083,8 +1104,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     }
 #pragma unroll
     for (int o = 4; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (k < last && e == 0) sc[k] = seen ? s : -INFINITY;
-    if (seen) top = fmaxf(top, s);
+    if (k < seen) {
+      if (e == 0) sc[k] = s;
+      top = fmaxf(top, s);
+    }
   }
 
   // the common reference of the splits and the draft, then the factors
@@ -1096,7 +1119,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
     fac[s] = f;
     if (f > 0.f) l = __fmaf_rn(f, part[static_cast<int64_t>(s) * kTreePart + 1], l);
   }
-  for (int k = lane; k < last; k += 32) {
+  for (int k = lane; k < seen; k += 32) {
     const float p = exp2f(sc[k] - ref);
     sc[k] = p;
     l += p;
@@ -1133,13 +1156,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
   o[3] = x1 - x3;
 
 #pragma unroll 4
-  for (int k = 0; k < last; ++k) {
+  for (int k = 0; k < seen; ++k) {
     const float p = sc[k];
-    if (p > 0.f) {
-      const __nv_bfloat16* v = Vn + k * L.vns.token + lane;
+    const __nv_bfloat16* v = Vn + list[k] * L.vns.token + lane;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = __fmaf_rn(p, __bfloat162float(v[32 * i]), o[i]);
-    }
+    for (int i = 0; i < 4; ++i) o[i] = __fmaf_rn(p, __bfloat162float(v[32 * i]), o[i]);
   }
   const float inv = sum > 0.f ? 1.0f / sum : 0.f;
   __nv_bfloat16* op = static_cast<__nv_bfloat16*>(L.out) + u * L.os.unit + j * L.os.head +
@@ -1152,12 +1173,18 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
 }
 
 // ------------------------------------------------------------------ launch
+constexpr int kTreeTileCost[4] = {31, 33, 41, 69};
+
 struct TreePlan {
   int cols, rblocks;
   int64_t tiles, per, nsplit;
 };
 
-// Rows per CTA: up to 128 columns, blocks of equal width for more rows.
+// Rows per CTA (columns of the products): the width whose blocks take the
+// least time together.  A tile takes 31, 33, 41 and 69 units with 16, 32, 64
+// and 128 columns (measured on 32 x 8 x 13 147 tokens: 306, 330, 405, 690 us of
+// this kernel; below 64 columns the keys are the work), so two blocks of 64
+// lose to one of 128, and three beat two of 128.
 // Splits: the launch costs (waves of 148 CTAs) * (tiles per CTA + setup, about
 // three tiles); the smallest cost, the fewest splits among equals.  Units that
 // may hold fewer than n tokens (their lengths are on the device) even out only
@@ -1166,10 +1193,16 @@ struct TreePlan {
 static TreePlan tree_plan(int units, int heads, int G, int nodes, int64_t n, bool ragged) {
   TreePlan p{};
   const int64_t rows = static_cast<int64_t>(nodes) * G;
-  p.rblocks = static_cast<int>((rows + 127) / 128);
-  const int64_t cols = (rows + p.rblocks - 1) / p.rblocks;
-  p.cols = cols <= 16 ? 16 : (cols <= 32 ? 32 : (cols <= 64 ? 64 : 128));
-  p.rblocks = static_cast<int>((rows + p.cols - 1) / p.cols);
+  int64_t least = -1;
+  for (int i = 0; i < 4; ++i) {
+    const int cols = 16 << i;
+    const int64_t blocks = (rows + cols - 1) / cols, cost = blocks * kTreeTileCost[i];
+    if (least < 0 || cost < least) {
+      least = cost;
+      p.cols = cols;
+      p.rblocks = static_cast<int>(blocks);
+    }
+  }
   p.tiles = (n + kTreeTile - 1) / kTreeTile;
   if (p.tiles < 1) p.tiles = 1;
   const int64_t ctas = static_cast<int64_t>(units) * heads * p.rblocks;
@@ -1263,7 +1296,7 @@ cudaError_t launch_tree_attend(const TreeLaunch& L, cudaStream_t stream) {
   }
   const int64_t rows = static_cast<int64_t>(L.units) * L.heads * a.rows;
   const int smem = kCombineWarps * combine_floats(static_cast<int>(a.nsplit), L.nodes) *
-                   static_cast<int>(sizeof(float));  // at most 28 KB
+                   static_cast<int>(sizeof(float));  // at most 44 KB
   tree_combine_kernel<<<static_cast<unsigned>((rows + kCombineWarps - 1) / kCombineWarps),
                         32 * kCombineWarps, smem, stream>>>(a);
   return cudaGetLastError();

@@ -531,6 +531,27 @@ def test_tree_sharp_flat_and_negative_scores(nq):
     check_tree(nq, 1, 2, 4, 8, 500, q_scale=2.0 ** 60, scale=2.0 ** -63, seed=15)
 
 
+@pytest.mark.parametrize("nodes,G,n,page,ragged", [
+    (1, 4, 40000, 0, False), (7, 4, 21001, 64, True), (16, 4, 30000, 0, True), (5, 3, 12345, 0, False),
+    (32, 4, 17000, 48, False), (24, 8, 26000, 0, True)])
+def test_tree_many_tiles_per_cta(nq, nodes, G, n, page, ragged):
+    """Long caches: many tiles pass through each CTA's pipeline (the barriers'
+    phases wrap many times).  Against the simple arithmetic in fp64 for one
+    head, repeated calls equal bit for bit, no wait run out."""
+    units = 3 if ragged else 2
+    lens = [n, n // 3, n - 129] if ragged else None
+    check_tree(nq, units, 1, G, nodes, n, P=page, lens=lens, seed=n)
+    ks, vs = fill_store(nq, 40, 8, 1500, 3, 1), fill_store(nq, 40, 8, 1500, 2, 2)
+    tab = nq.rope_tables(1e4, 1500)
+    g = gen(n)
+    q = torch.randn(40, 8 * G, nodes, D, generator=g, device="cuda").to(torch.bfloat16)
+    Kn = torch.randn(40, 8, nodes, D, generator=g, device="cuda").to(torch.bfloat16)
+    first = nq.nq_tree_attend(q, Kn, Kn, ks, vs, 1500, tab, 1500)
+    for _ in range(20):
+        assert torch.equal(nq.nq_tree_attend(q, Kn, Kn, ks, vs, 1500, tab, 1500), first)
+    assert nq.device_error() == 0
+
+
 def test_tree_value_and_key_scales(nq):
     """fp16 scales far from one (values are averaged in scaled codes)."""
     check_tree(nq, 1, 2, 4, 8, 400, sigma_v=1000.0, seed=16)

@@ -791,7 +791,7 @@ nq_status nq_tree_attend(const void* q, nq_kv_strides qs, const void* K_new, nq_
     L.k_in = *k_in;
     L.v_in = *v_in;
   }
-  L.n = n;
+  L.n = table && pages == 0 ? 0 : n;  // no page exists: every token is left out
   L.lens = lens;
   L.table = table;
   L.table_stride = table_stride;

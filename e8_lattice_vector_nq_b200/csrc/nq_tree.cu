@@ -99,11 +99,13 @@ __global__ void __launch_bounds__(kAngleThreads) tree_angles_kernel(const TreeAr
     if (lane < kPer && tok < a.L.n) {
       const int32_t p = a.L.positions ? __ldg(a.L.positions + u * a.L.pos_stride + tok)
                                       : static_cast<int32_t>(tok);
-      mine = a.L.pos_base + (p < 0 ? 0 : p);  // out-of-contract positions stay in bounds
+      mine = a.L.pos_base + (p < 0 ? 0 : p);
     }
   }
+  // out-of-contract positions stay in bounds
+  mine = min64(mine, min64(a.n_a * 256 - 1, 0x7FFFFFFF));
   const float4* tab = reinterpret_cast<const float4*>(a.L.rope_tab);
-  const int pos32 = static_cast<int>(mine);  // below 2^31: the ABI layer checks
+  const int pos32 = static_cast<int>(mine);
   // eight fine rows in flight; nearby positions share the coarse row, which is
   // read again only when it changes
   int64_t row = -1;
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kAngleThreads) tree_angles_kernel(const TreeAr
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t hi = min64(pos[i] >> 8, a.n_a - 1);
+      const int64_t hi = pos[i] >> 8;
       if (hi != row) A = __ldg(tab + hi * 32 + lane);
       row = hi;
       const float c0 = __fmaf_rn(A.x, B[i].x, -__fmul_rn(A.y, B[i].y));

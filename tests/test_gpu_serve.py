@@ -517,6 +517,38 @@ def test_tree_missing_pages_are_left_out(nq):
     check_tree(nq, 2, 2, 4, 3, 200, P=16, hole=(1, slice(None)), kind="sparse", seed=6)
 
 
+def test_tree_bad_positions_and_empty_batches(nq):
+    """Positions past the table (out of contract) read some row of it and fault
+    nothing; a batch of no units and a pool of no pages are accepted."""
+    ks, vs = fill_store(nq, 1, 2, 200, 3, 1), fill_store(nq, 1, 2, 200, 2, 2)
+    tab = nq.rope_tables(1e4, 300)
+    z = lambda u: torch.randn(u, 2, 3, D, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, K = z(1), z(1)
+    bad = torch.full((1, 200), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    bad[0, ::2] = -(2 ** 31)
+    for base in (0, 250):
+        out = nq.nq_tree_attend(q, K, K, ks, vs, 200, tab, 300, positions=bad, pos_base=base)
+        assert torch.isfinite(out).all()
+    qk = nq.nq_qk_norm_rope(q, K, tab, 300, positions=bad[:, :3], pos_base=7)
+    assert torch.isfinite(qk[0]).all()
+    nq.nq_encode_slots(K[0], K[0], ks, vs, i32([1, 2, 3]), bad[0, :3], tab, 300)
+    none = nq.nq_tree_attend(z(0), z(0), z(0), ks, vs, 200, tab, 300)
+    assert none.shape == (0, 2, 3, D)
+    torch.cuda.synchronize()
+    # through the C interface: a pool of no pages leaves the draft alone
+    L, p = nq.lib(), lambda t: ctypes.c_void_p(t.data_ptr())
+    out, want = torch.empty_like(q), nq.nq_tree_attend(q, K, K, None, None, 0)
+    ws = nq.tree_attend_workspace(1, 2, 1, 3, 200)
+    st = lambda t: nq.KVStrides(*t.stride()[:3])  # noqa: E731
+    kd, vd, tb = ks.desc(), vs.desc(), i32([[0, 0]])
+    status = L.nq_tree_attend(p(q), st(q), p(K), st(K), p(K), st(K), 1, 2, 1, 3, ctypes.byref(kd),
+                              ctypes.byref(vd), 200, None, p(tb), 2, 100, 0, None, 0, 0, p(tab), 300,
+                              None, 0, D ** -0.5, p(out), st(out), None, p(ws),
+                              ws.numel() * 4, None)
+    torch.cuda.synchronize()
+    assert status == 0 and torch.equal(out, want)
+
+
 def test_tree_kept_positions_base_and_layout(nq):
     check_tree(nq, 2, 8, 4, 9, 700, kept=True, theta=1e6, seed=7)
     check_tree(nq, 2, 4, 7, 9, 700, kept=True, pos_base=60000, theta=1e6, layout="head", seed=8)

@@ -37,12 +37,14 @@
  *   contract (no fault: the kernels stay within their buffers, the codes of
  *   such a vector are unspecified).
  * - Staging uses cp.async groups and bulk-copy groups, whose waits complete
- *   in hardware.  The one polled wait is decode's wait for its own
- *   tensor-core products (an mbarrier that the MMA unit signals on
- *   completion); it is bounded (2^20 polls), and when it expires the kernel
- *   sets bit 1 of the device error word and its warpgroup stops (that call's
- *   output is then incomplete).  nq_device_error() reads the device error
- *   word; it reads 0 after any sequence of valid calls.
+ *   in hardware.  The polled waits are decode's wait for its own tensor-core
+ *   products (an mbarrier that the MMA unit signals on completion) and the
+ *   waits of nq_tree_attend's warpgroups for one another and for their
+ *   products; all are bounded (2^20 polls).  When one expires, the kernel sets
+ *   bit 1 (decode: its warpgroup stops, the output is then incomplete) or bit
+ *   2 (tree attention: it runs through without waiting, the output is then
+ *   unspecified) of the device error word.  nq_device_error() reads that word;
+ *   it reads 0 after any sequence of valid calls.
  */
 #ifndef NQ_H
 #define NQ_H

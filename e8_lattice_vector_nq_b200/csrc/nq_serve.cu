@@ -214,16 +214,17 @@ struct NormRaw {
   uint4 v[F32 ? 4 : 2];
 };
 
+// Asynchronous copy of the lane's share into its own slots of a ring stage
+// (chunk c of thread i at c * kNormThreads * 16 + i * 16: nothing is shared
+// between threads, so each waits for its own copies only).
 template <bool F32>
-__device__ __forceinline__ void norm_load(const void* p, int64_t off, int l, NormRaw<F32>& r) {
-  if constexpr (F32) {
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + off);
+__device__ __forceinline__ void norm_fetch(const void* p, int64_t off, int l, uint32_t dst) {
+  constexpr int kChunks = F32 ? 4 : 2;
+  const char* s = static_cast<const char*>(p) + off * (F32 ? 4 : 2);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) r.v[c] = __ldcs(s + (c < 2 ? 2 * l + c : 16 + 2 * l + c - 2));
-  } else {
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + off);
-    r.v[0] = __ldcs(s + l);
-    r.v[1] = __ldcs(s + l + 8);
+  for (int c = 0; c < kChunks; ++c) {
+    const int chunk = F32 ? (c < 2 ? 2 * l + c : 16 + 2 * l + c - 2) : l + 8 * c;
+    cp_async16(dst + c * (kNormThreads * 16), s + chunk * 16);
   }
 }
 
@@ -268,7 +269,11 @@ __device__ __forceinline__ void norm_store(void* p, int64_t off, int l, bool f32
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kNormThreads, 2) norm_rope_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, 3) norm_rope_kernel(const NormArgs a) {
+  // Stages of a head each, all but one under way: 3 CTAs x 256 threads x 4 x 32
+  // bytes = 98 KB per SM (fp32: 49 KB).
+  constexpr int kStages = F32 ? 2 : 5, kStage = (F32 ? 4 : 2) * kNormThreads * 16;
+  extern __shared__ __align__(16) unsigned char norm_smem[];
   __shared__ __align__(16) float weights[2][kD];  // of the queries, of the keys
   const NormRopeLaunch& L = a.L;
   {
@@ -302,31 +307,30 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_kernel(const NormAr
   const int h0 = chunk * a.per, h1 = min(h0 + a.per, heads);
   // the groups of a warp may run different numbers of heads: each shuffles alone
   const uint32_t lanes = 0xFFu << (threadIdx.x & 24);
-  constexpr int kU = F32 ? 1 : 2;  // heads per step; those of the next step are in flight
-  NormRaw<F32> next[kU];
+  const uint32_t ring = smem_u32(norm_smem) + threadIdx.x * 16;
   auto fetch = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int hh = min(h + i, h1 - 1);
-      if (hh < L.q_heads)
-        norm_load<F32>(L.q, u * L.qs.unit + hh * L.qs.head + t * L.qs.token, l, next[i]);
+    if (h < h1) {
+      const uint32_t dst = ring + ((h - h0) % kStages) * kStage;
+      if (h < L.q_heads)
+        norm_fetch<F32>(L.q, u * L.qs.unit + h * L.qs.head + t * L.qs.token, l, dst);
       else
-        norm_load<F32>(L.k, u * L.ks.unit + (hh - L.q_heads) * L.ks.head + t * L.ks.token, l, next[i]);
+        norm_fetch<F32>(L.k, u * L.ks.unit + (h - L.q_heads) * L.ks.head + t * L.ks.token, l, dst);
     }
+    cp_async_commit();
   };
-  fetch(h0);
-  for (int h = h0; h < h1; h += kU) {
-    NormRaw<F32> cur[kU];
 #pragma unroll
-    for (int i = 0; i < kU; ++i) cur[i] = next[i];
-    if (h + kU < h1) fetch(h + kU);
-#pragma unroll
-    for (int i = 0; i < kU; ++i) {
-      const int hh = h + i;
-      if (hh >= h1) break;
+  for (int i = 0; i < kStages - 1; ++i) fetch(h0 + i);
+  for (int hh = h0; hh < h1; ++hh) {
+    fetch(hh + kStages - 1);  // into the stage that the last head left
+    cp_async_wait<kStages - 1>();
+    {
       const bool is_q = hh < L.q_heads;
+      NormRaw<F32> raw;
+      const uint32_t src = ring + ((hh - h0) % kStages) * kStage;
+#pragma unroll
+      for (int c2 = 0; c2 < (F32 ? 4 : 2); ++c2) raw.v[c2] = lds128(src + c2 * (kNormThreads * 16));
       float x[16], o[16];
-      norm_floats<F32>(cur[i], x);
+      norm_floats<F32>(raw, x);
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) ss = __fmaf_rn(x[e], x[e], ss);
@@ -370,10 +374,12 @@ cudaError_t launch_norm_rope(const NormRopeLaunch& L, cudaStream_t stream) {
   a.items = tokens * a.chunks;
   const int64_t grid = (a.items * 8 + kNormThreads - 1) / kNormThreads;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  // shared bytes of the rings, within the 48 KB that need no attribute
+  constexpr int kRow = kNormThreads * 16;
   if (L.in_f32)
-    norm_rope_kernel<true><<<static_cast<unsigned>(grid), kNormThreads, 0, stream>>>(a);
+    norm_rope_kernel<true><<<static_cast<unsigned>(grid), kNormThreads, 2 * 4 * kRow, stream>>>(a);
   else
-    norm_rope_kernel<false><<<static_cast<unsigned>(grid), kNormThreads, 0, stream>>>(a);
+    norm_rope_kernel<false><<<static_cast<unsigned>(grid), kNormThreads, 5 * 2 * kRow, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kAngleThreads) tree_angles_kernel(const TreeAr
   const int pos32 = static_cast<int>(mine);
   // eight fine rows in flight; nearby positions share the coarse row, which is
   // read again only when it changes
-  int64_t row = -1;
-  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  int64_t row = __shfl_sync(0xffffffffu, pos32, 0) >> 8;
+  float4 A = __ldg(tab + row * 32 + lane);
 #pragma unroll
   for (int i0 = 0; i0 < kPer; i0 += 8) {
     float4 B[8];
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kAngleThreads) tree_angles_kernel(const TreeAr
 // 32 consecutive codes as 16 f16 pairs.  A code sits in the mantissa of an f16
 // whose exponent is that of 1024, at bit d >= 1 (1024 + j 2^d), two codes 16
 // bits apart per register, so one AND-OR turns a shifted view of the words
-// into a pair and one exact fma into 2j - (2^b - 2):
+// into a pair and one exact fma into t = 2j - (2^b - 2) - h:
 //   b = 3: pairs (a, a+5) of each run of ten codes (15 bits apart: d differs
 //          by one between the lanes), the last pair (30, 31) from its own bits;
 //   b = 2: pairs (i, i+8) of each word.
@@ -179,9 +179,9 @@ __host__ __device__ constexpr uint32_t f16_bits(float v) {
 }
 __host__ __device__ constexpr uint32_t f16_pair(float lo, float hi) { return f16_bits(lo) | (f16_bits(hi) << 16); }
 
-__device__ __forceinline__ uint32_t hadd2u(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 __device__ __forceinline__ uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
@@ -202,31 +202,41 @@ __device__ __forceinline__ uint32_t coset_mask(uint32_t z, int ga, int gb) {
   return m;
 }
 
-// The pair with fields at bits dl (low lane) and 16 + dh of v -> 2j - (2^b - 2).
+// The pair with fields at bits dl (low lane) and 16 + dh of v -> 2j - (2^b - 2)
+// - h, h the lanes' coset bits as a mask.  The addend -(1024 * 2^(1-d) + 2^b - 2)
+// has a zero bit where 1.0 is added to its magnitude (2^b - 2 is even and small
+// against the power of two), so an OR takes h off.
 template <int BITS, int DL, int DH>
-__device__ __forceinline__ uint32_t tree_pair(uint32_t v) {
+__device__ __forceinline__ uint32_t tree_pair(uint32_t v, uint32_t hmask) {
   constexpr uint32_t kMask = (((1u << BITS) - 1u) << DL) | (((1u << BITS) - 1u) << (16 + DH));
   constexpr float kOff = static_cast<float>((1 << BITS) - 2);
   constexpr float kScaleL = 2.0f / (1 << DL), kScaleH = 2.0f / (1 << DH);
   constexpr uint32_t kMul = f16_pair(kScaleL, kScaleH);
   constexpr uint32_t kAdd = f16_pair(-(1024.0f * kScaleL + kOff), -(1024.0f * kScaleH + kOff));
-  return hfma2u((v & kMask) | 0x64006400u, kMul, kAdd);
+  constexpr uint32_t kAdd1 = f16_pair(-(1024.0f * kScaleL + kOff + 1.0f), -(1024.0f * kScaleH + kOff + 1.0f));
+  static_assert((kAdd1 & kAdd) == kAdd, "the coset bit is an OR");
+  return hfma2u((v & kMask) | 0x64006400u, kMul, kAdd | (hmask & (kAdd1 ^ kAdd)));
 }
 
 template <int BITS>
-__device__ __forceinline__ void tree_unpack(const uint32_t (&w)[BITS], uint32_t (&h)[16]) {
+__device__ __forceinline__ void tree_unpack(const uint32_t (&w)[BITS], uint32_t cosets,
+                                            uint32_t (&h)[16]) {
+  const uint32_t z = coset_bytes(cosets);
+  auto hm = [&](int q) {
+    return coset_mask(z, tree_slot<BITS>(2 * q) >> 3, tree_slot<BITS>(2 * q + 1) >> 3);
+  };
   if constexpr (BITS == 2) {
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const uint32_t v0 = w[m] << 1, v1 = w[m] >> 7;
-      h[8 * m] = tree_pair<2, 1, 1>(v0);
-      h[8 * m + 1] = tree_pair<2, 3, 3>(v0);
-      h[8 * m + 2] = tree_pair<2, 5, 5>(v0);
-      h[8 * m + 3] = tree_pair<2, 7, 7>(v0);
-      h[8 * m + 4] = tree_pair<2, 1, 1>(v1);
-      h[8 * m + 5] = tree_pair<2, 3, 3>(v1);
-      h[8 * m + 6] = tree_pair<2, 5, 5>(v1);
-      h[8 * m + 7] = tree_pair<2, 7, 7>(v1);
+      h[8 * m] = tree_pair<2, 1, 1>(v0, hm(8 * m));
+      h[8 * m + 1] = tree_pair<2, 3, 3>(v0, hm(8 * m + 1));
+      h[8 * m + 2] = tree_pair<2, 5, 5>(v0, hm(8 * m + 2));
+      h[8 * m + 3] = tree_pair<2, 7, 7>(v0, hm(8 * m + 3));
+      h[8 * m + 4] = tree_pair<2, 1, 1>(v1, hm(8 * m + 4));
+      h[8 * m + 5] = tree_pair<2, 3, 3>(v1, hm(8 * m + 5));
+      h[8 * m + 6] = tree_pair<2, 5, 5>(v1, hm(8 * m + 6));
+      h[8 * m + 7] = tree_pair<2, 7, 7>(v1, hm(8 * m + 7));
     }
   } else {
     auto window = [&](int s) -> uint32_t {  // bits [s, s + 32) of the 96
@@ -238,13 +248,13 @@ __device__ __forceinline__ void tree_unpack(const uint32_t (&w)[BITS], uint32_t 
 #pragma unroll
     for (int b = 0; b < 3; ++b) {
       const uint32_t v0 = window(30 * b - 2), v1 = window(30 * b + 4), v2 = window(30 * b + 10);
-      h[5 * b] = tree_pair<3, 2, 1>(v0);
-      h[5 * b + 1] = tree_pair<3, 5, 4>(v0);
-      h[5 * b + 2] = tree_pair<3, 2, 1>(v1);
-      h[5 * b + 3] = tree_pair<3, 5, 4>(v1);
-      h[5 * b + 4] = tree_pair<3, 2, 1>(v2);
+      h[5 * b] = tree_pair<3, 2, 1>(v0, hm(5 * b));
+      h[5 * b + 1] = tree_pair<3, 5, 4>(v0, hm(5 * b + 1));
+      h[5 * b + 2] = tree_pair<3, 2, 1>(v1, hm(5 * b + 2));
+      h[5 * b + 3] = tree_pair<3, 5, 4>(v1, hm(5 * b + 3));
+      h[5 * b + 4] = tree_pair<3, 2, 1>(v2, hm(5 * b + 4));
     }
-    h[15] = tree_pair<3, 2, 1>(((w[2] >> 24) & 0x1Cu) | ((w[2] >> 12) & 0xE0000u));
+    h[15] = tree_pair<3, 2, 1>(((w[2] >> 24) & 0x1Cu) | ((w[2] >> 12) & 0xE0000u), hm(15));
   }
 }
 
@@ -384,9 +394,12 @@ struct TokenWalk {
     if (row && t < t1) page = __ldg(row + fdiv(t, div));
   }
   __device__ __forceinline__ void next(int32_t& lead, uint32_t& slot) {
-    const bool ok = t < t1 && (!row || (page >= 0 && page < pages));
-    lead = ok ? page : -1;
-    slot = row ? t - fdiv(t, div) * div.d : t;
+    lead = t < t1 ? page : -1;
+    slot = t;
+    if (row) {  // (uniform: a contiguous unit costs none of this)
+      if (page < 0 || page >= pages) lead = -1;
+      slot = t - fdiv(t, div) * div.d;
+    }
     t += kTreeTile;
     fetch();
   }
@@ -595,12 +608,7 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
         for (int i = 0; i < BK; ++i)
           w[i] = !kChunks ? wd[s * BK + i]
                           : (kw == 0 ? wd[i] : (kw == 1 ? wd[i + 3] : (kw == 2 ? wd[i + 2] : wd[i + 1])));
-        tree_unpack<BK>(w, hh);
-        const uint32_t z = coset_bytes(meta >> (4 * run));
-#pragma unroll
-        for (int q = 0; q < 16; ++q)  // - h (-1.0 = 0xBC00), exact
-          hh[q] = hadd2u(hh[q], 0xBC00BC00u & coset_mask(z, tree_slot<BK>(2 * q) >> 3,
-                                                         tree_slot<BK>(2 * q + 1) >> 3));
+        tree_unpack<BK>(w, meta >> (4 * run), hh);
         tmem_st(S::tT + t_lane + 16 * run, hh);
       }
       if (kw == KW - 2) {
@@ -712,18 +720,15 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
       value_scale(meta, m, e);
       const uint32_t s16 = __half_as_ushort(
           __float2half_rn(__uint_as_float(static_cast<uint32_t>(125 + e) << 23)));
-      const uint32_t ss = s16 | (s16 << 16), neg = ss ^ 0x80008000u;
+      const uint32_t ss = s16 | (s16 << 16);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {  // 32 codes at a time
         uint32_t x[BV], hh[16];
 #pragma unroll
         for (int i = 0; i < BV; ++i) x[i] = wd[w * BV + i];
-        tree_unpack<BV>(x, hh);
-        const uint32_t z = coset_bytes(meta >> (4 * w));
+        tree_unpack<BV>(x, meta >> (4 * w), hh);
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
-          hh[q] = hfma2u(hh[q], ss, neg & coset_mask(z, tree_slot<BV>(2 * q) >> 3,
-                                                     tree_slot<BV>(2 * q + 1) >> 3));
+        for (int q = 0; q < 16; ++q) hh[q] = hmul2u(hh[q], ss);
         const uint32_t dst = base + S::V + (j & 1) * 32768 + (w >> 1) * 16384;
 #pragma unroll
         for (int c = 0; c < 4; ++c)

@@ -590,6 +590,21 @@ def _strides4(t: torch.Tensor, types, name: str) -> KVStrides:
     return KVStrides(a if u > 1 else 0, b if h > 1 else 0, c if r > 1 else 0)
 
 
+def _contiguous4(t: torch.Tensor) -> KVStrides:
+    """Strides of a [units, heads, rows, 128] tensor just allocated."""
+    _, h, r, d = t.shape
+    return KVStrides(h * r * d, r * d, d)
+
+
+def _packed(s: PackedStore) -> Packed:
+    """PackedStore.desc with one check."""
+    u, h, _ = s.meta.stride()
+    w = 4 * s.bits
+    if s.codes.stride()[:2] != (u * w, h * w):
+        raise ValueError("codes and meta of a store must be laid out alike")
+    return Packed(s.codes.data_ptr(), s.meta.data_ptr(), u, h, s.bits)
+
+
 def _addr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -609,7 +624,7 @@ class PageTables:
     @classmethod
     def empty(cls, requests: int, max_rows: int, device="cuda") -> "PageTables":
         e = torch.empty(2 * max_rows + 2 * requests + 3, dtype=torch.int32, device=device)
-        slots, pos, lens, starts, used = e.split(
+        slots, pos, lens, starts, used = e.split_with_sizes(
             (max_rows, max_rows, requests, requests + 1, 2))
         return cls(lens, starts, slots, pos, used)
 
@@ -683,18 +698,22 @@ def nq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope_tab: to
         if q is not None:
             qs, hq = _strides4(q, _TYPES, "q"), q.shape[1]
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q_dtype or q.dtype, device=q.device)
+                q_out = q.new_empty(q.shape, dtype=q_dtype)
+                qos = _contiguous4(q_out)
             elif q_out.shape != q.shape or (q_dtype is not None and q_dtype != q_out.dtype):
                 raise ValueError("q_out must have the shape of q and the type asked for")
-            qos = _strides4(q_out, _TYPES, "q_out")
+            else:
+                qos = _strides4(q_out, _TYPES, "q_out")
             qt = _TYPES[q_out.dtype]
         if k is not None:
             ks, hk = _strides4(k, _TYPES, "k"), k.shape[1]
             if k_out is None:
-                k_out = torch.empty(k.shape, dtype=k_dtype or k.dtype, device=k.device)
+                k_out = k.new_empty(k.shape, dtype=k_dtype)
+                kos = _contiguous4(k_out)
             elif k_out.shape != k.shape or (k_dtype is not None and k_dtype != k_out.dtype):
                 raise ValueError("k_out must have the shape of k and the type asked for")
-            kos = _strides4(k_out, _TYPES, "k_out")
+            else:
+                kos = _strides4(k_out, _TYPES, "k_out")
             kt = _TYPES[k_out.dtype]
         _check(lib().nq_qk_norm_rope(_addr(q), qs, hq, _addr(k), ks, hk, _TYPES[ref.dtype], units,
                                      rows, _addr(q_weight), _addr(k_weight), eps, _addr(positions),
@@ -737,7 +756,7 @@ def nq_encode_slots(K: torch.Tensor | None, V: torch.Tensor | None, k_out: Packe
         shape = shape or s.meta.shape
         if s.meta.shape != shape or shape[1] != heads or s.meta.get_device() != idx:
             raise ValueError("the stores must be [pages][heads][page_size] alike, on the tensors' device")
-        desc.append(ctypes.byref(s.desc()))
+        desc.append(_packed(s))
         strides.append(KVStrides(0, t.stride(0) if heads > 1 else 0, t.stride(1) if rows > 1 else 0))
     if rows == 0:  # an empty tensor has no address
         return
@@ -814,7 +833,7 @@ def nq_tree_attend(q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
             ps = _positions(positions, units, n)
             if units > 1 and ps < n:
                 raise ValueError("positions rows overlap")
-        kd, vd = ctypes.byref(k_in.desc()), ctypes.byref(v_in.desc())
+        kd, vd = _packed(k_in), _packed(v_in)
     else:
         table = positions = None
     if lens is not None:
@@ -830,21 +849,24 @@ def nq_tree_attend(q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
     st, ctx = _stream_on(idx, stream)
     with ctx:
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            out = q.new_empty(q.shape)
+            os_ = _contiguous4(out)
         elif out.shape != q.shape:
             raise ValueError("out must have the shape of q")
-        lse_t = torch.empty(units, Hq, nodes, dtype=torch.float32, device=q.device) if lse else None
+        else:
+            os_ = _strides4(out, bf, "out")
+        lse_t = q.new_empty((units, Hq, nodes), dtype=torch.float32) if lse else None
         if ws is None:
             need = L.nq_tree_attend_workspace_bytes(units, heads, G, nodes, n, positions is None,
                                                     lens is not None)
-            ws = torch.empty(need // 4 + 4, dtype=torch.float32, device=q.device)
+            ws = q.new_empty(need // 2 + 8)
         elif not ws.is_contiguous():
             raise ValueError("ws must be contiguous")
         _check(L.nq_tree_attend(
             q.data_ptr(), qs, K_new.data_ptr(), kns, V_new.data_ptr(), vns, units, heads, G, nodes,
             kd, vd, n, _addr(lens), _addr(table), tstride, page, pages, _addr(positions), ps,
             pos_base, _addr(rope_tab), rope_max_pos, _addr(mask), ms,
-            D ** -0.5 if scale is None else scale, out.data_ptr(), _strides4(out, bf, "out"),
+            D ** -0.5 if scale is None else scale, out.data_ptr(), os_,
             _addr(lse_t), ws.data_ptr(), ws.numel() * ws.element_size(), st))
     return (out, lse_t) if lse else out
 

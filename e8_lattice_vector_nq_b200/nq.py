@@ -590,6 +590,12 @@ def _strides4(t: torch.Tensor, types, name: str) -> KVStrides:
     return KVStrides(a if u > 1 else 0, b if h > 1 else 0, c if r > 1 else 0)
 
 
+def _type(t: torch.Tensor) -> int:
+    if t.dtype not in _TYPES:
+        raise ValueError(f"{t.dtype} is not an output type: bfloat16 or float32")
+    return _TYPES[t.dtype]
+
+
 def _contiguous4(t: torch.Tensor) -> KVStrides:
     """Strides of a [units, heads, rows, 128] tensor just allocated."""
     _, h, r, d = t.shape
@@ -603,6 +609,13 @@ def _packed(s: PackedStore) -> Packed:
     if s.codes.stride()[:2] != (u * w, h * w):
         raise ValueError("codes and meta of a store must be laid out alike")
     return Packed(s.codes.data_ptr(), s.meta.data_ptr(), u, h, s.bits)
+
+
+def _rope_table(t: torch.Tensor, max_pos: int) -> None:
+    """Tables of rope_tables() for at least max_pos positions (a shorter one
+    would be read past its end): rows of 64 (cos, sin) pairs."""
+    if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() < ((max_pos + 255) // 256 + 256) * D:
+        raise ValueError(f"rope_tab is not the float32 table of {max_pos} positions")
 
 
 def _addr(t: torch.Tensor | None):
@@ -687,6 +700,7 @@ def nq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope_tab: to
                            or q.shape[2] != k.shape[2] or q.dtype != k.dtype)):
         raise ValueError("q and k must be [units, heads, rows, 128] of the same units, rows and type")
     units, _, rows, _ = ref.shape
+    _rope_table(rope_tab, rope_max_pos)
     for w in (q_weight, k_weight):
         if w is not None and (w.dtype != torch.float32 or w.shape != (D,) or w.stride(0) != 1):
             raise ValueError("weights must be float32 [128]")
@@ -704,7 +718,7 @@ def nq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope_tab: to
                 raise ValueError("q_out must have the shape of q and the type asked for")
             else:
                 qos = _strides4(q_out, _TYPES, "q_out")
-            qt = _TYPES[q_out.dtype]
+            qt = _type(q_out)
         if k is not None:
             ks, hk = _strides4(k, _TYPES, "k"), k.shape[1]
             if k_out is None:
@@ -714,7 +728,7 @@ def nq_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope_tab: to
                 raise ValueError("k_out must have the shape of k and the type asked for")
             else:
                 kos = _strides4(k_out, _TYPES, "k_out")
-            kt = _TYPES[k_out.dtype]
+            kt = _type(k_out)
         _check(lib().nq_qk_norm_rope(_addr(q), qs, hq, _addr(k), ks, hk, _TYPES[ref.dtype], units,
                                      rows, _addr(q_weight), _addr(k_weight), eps, _addr(positions),
                                      ps, pos_base, rope_tab.data_ptr(), rope_max_pos,
@@ -741,6 +755,8 @@ def nq_encode_slots(K: torch.Tensor | None, V: torch.Tensor | None, k_out: Packe
     _int32(slots, (rows,), "slots")
     if K is not None and positions is None:
         raise ValueError("keys need positions")
+    if K is not None and rope_tab is not None:
+        _rope_table(rope_tab, rope_max_pos)
     if positions is not None:
         _int32(positions, (rows,), "positions")
     shape, desc, strides = None, [], []
@@ -809,6 +825,7 @@ def nq_tree_attend(q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
     if n > 0:
         if k_in is None or v_in is None or rope_tab is None:
             raise ValueError("n > 0 needs k_in, v_in and rope_tab")
+        _rope_table(rope_tab, rope_max_pos)
         lead, h, cap = k_in.meta.shape
         if v_in.meta.shape != (lead, h, cap) or h != heads:
             raise ValueError("k_in and v_in must be [units or pages][heads][slots] alike")
@@ -1125,17 +1142,21 @@ class PagedStore:
 
     A prompt is the same with its own counts.  Tokens sit at their positions
     (token t of a request at RoPE position t).  plan() changes nothing but
-    fresh table entries, so a plan may be dropped and made again."""
+    fresh table entries, so a plan may be dropped and made again (before
+    commit() a server looks at plan.used[1]: pages or rows may have run out)."""
 
     def __init__(self, requests: int, layers: int, heads: int, pages: int, page_size: int,
                  max_tokens: int, theta: float, bits_k: int = 3, bits_v: int = 2, device="cuda"):
-        self.S, self.L, self.H, self.P, self.n = requests, layers, heads, page_size, max_tokens
-        self.rope = rope_tables(theta, max_tokens, device)
+        # a request's pages are whole: max_tokens is rounded up to them, so that
+        # every token with a slot is attended
+        width = (max_tokens + page_size - 1) // page_size
+        self.S, self.L, self.H, self.P, self.n = requests, layers, heads, page_size, width * page_size
+        self.rope = rope_tables(theta, self.n, device)
         self.k = PackedStore.empty(layers * pages, heads, page_size, bits_k, device)
         self.v = PackedStore.empty(layers * pages, heads, page_size, bits_v, device)
         self.pages = pages
         e = lambda *s, fill: torch.full(s, fill, dtype=torch.int32, device=device)  # noqa: E731
-        self.table = e(requests, (max_tokens + page_size - 1) // page_size, fill=-1)
+        self.table = e(requests, width, fill=-1)
         self.lens, self.taken = e(requests, fill=0), e(1, fill=0)
         self.free = torch.arange(pages, dtype=torch.int32, device=device)
 

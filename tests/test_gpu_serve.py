@@ -741,6 +741,47 @@ def test_binding_refuses_wrong_shapes(nq):
         nq.nq_page_tables(i32([1]), i32([1, 2]), 16, i32([0]), i32([[0]]), 4)
 
 
+def test_binding_refuses_short_tables_and_other_types(nq):
+    """A table of angles for fewer positions than the call names would be read
+    past its end; an output type that the library does not write."""
+    ks, vs = nq.PackedStore.empty(2, 4, 512, 3), nq.PackedStore.empty(2, 4, 512, 2)
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q, K = z(2, 8, 5, D), z(2, 4, 5, D)
+    good = nq.rope_tables(1e4, 512)
+    for tab, most in ((good[:-1], 512), (good, 513), (good.double(), 512), (good.half(), 512)):
+        with pytest.raises(ValueError):
+            nq.nq_qk_norm_rope(q, K, tab, most)
+        with pytest.raises(ValueError):
+            nq.nq_encode_slots(K[0], K[0], ks, vs, i32([0] * 5), i32([1] * 5), tab, most)
+        with pytest.raises(ValueError):
+            nq.nq_tree_attend(q, K, K, ks, vs, 500, tab, most)
+    for kw in (dict(q_dtype=torch.float16), dict(k_dtype=torch.float64)):
+        with pytest.raises(ValueError):
+            nq.nq_qk_norm_rope(q, K, good, 512, **kw)
+
+
+def test_paged_store_rounds_up_to_whole_pages(nq):
+    """Every token that gets a slot is attended: a request of 23 tokens in pages
+    of 16, asked for with max_tokens = 20, has room for 32."""
+    store = nq.PagedStore(2, 1, 1, 5, 16, 20, 1e4)
+    assert store.n == 32
+    plan = store.plan(i32([23, 33]), 60)
+    assert plan.used.tolist() == [4, 2]  # the second request's 33rd token has no page
+    g = gen(77)
+    x = torch.randn(2, 1, 60, D, generator=g, device="cuda").to(torch.bfloat16)
+    store.write(0, x[0], x[1], plan.slots, plan.positions)
+    store.commit(plan)
+    q = torch.randn(2, 1, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    mask = torch.zeros(1, 1, dtype=torch.int64, device="cuda")  # the draft is not seen
+    _, lse = store.attend(0, torch.zeros_like(q), q, q, mask, lse=True)
+    # a query of zeros: log(tokens), computed as (log2(2^4 tokens) - 4) ln 2.  The
+    # logarithm (8.5 and 9, 1 ulp = 2^-20), the difference and the product (half
+    # an ulp, 2^-23 each) and ln 2 (2^-25 relative): below 2^-20, and as much
+    # again for the expected value's own rounding
+    want = torch.tensor([23.0, 32.0], dtype=torch.float64).log()
+    assert torch.allclose(lse.flatten().cpu().double(), want, rtol=0, atol=2.0 ** -19)
+
+
 # ----------------------------------------------------------- the run of them
 @pytest.mark.parametrize("captured", [False, True])
 def test_speculative_steps_over_a_paged_store(nq, captured):

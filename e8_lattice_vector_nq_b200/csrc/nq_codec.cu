@@ -1543,7 +1543,9 @@ cudaError_t launch_encode(const EncodeLaunch& L, cudaStream_t stream) {
   return cudaSuccess;
 }
 
-// One side (keys with RoPE, or values) of nq_encode_slots.
+// One side (keys with RoPE, or values) of nq_encode_slots.  Bound by the
+// instructions of the E8 search, as nq_encode is: 8191 rows x 8 heads, 3-bit
+// keys 23.5 us and 2-bit values 18 us; 64 rows 9 + 7 us, a launch's latency.
 template <int BITS, bool ROPE>
 static cudaError_t launch_slots(CodecArgs a, cudaStream_t stream) {
   a.hg = pick_head_group(a.heads);

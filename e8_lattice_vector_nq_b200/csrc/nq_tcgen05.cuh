@@ -271,16 +271,6 @@ __device__ __forceinline__ uint32_t elect_lane() {
   return on;
 }
 
-// MN-major operand in the 128-byte swizzled layout: one row of 128 bytes (64
-// 16-bit elements along M or N) per k, groups of 8 k 1024 bytes apart, the
-// next 64 elements of M or N lbo bytes on (16-byte chunk c of row k stored at
-// chunk c ^ (k % 8)); 1024-byte aligned groups.
-__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t lbo) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
-         (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(2) << 61);
-}
 // Instruction descriptor bits of MN-major A and B operands.
 constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 
@@ -288,14 +278,6 @@ constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("{\n\t.reg .b64 s;\n\tmbarrier.arrive.shared::cta.b64 s, [%0];\n\t}" ::"r"(bar)
                : "memory");
-}
-// One arrival of this thread once its cp.async copies so far have landed.
-__device__ __forceinline__ void mbar_arrive_cp_async(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-// Arrival without waiting at a named barrier over `count` threads.
-__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t count) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 // OR of pred over the `count` threads of named barrier `id`.
 __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool pred) {

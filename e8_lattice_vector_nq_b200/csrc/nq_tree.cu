@@ -6,7 +6,7 @@
 // tensor cores with the TOKENS as the 128 rows of the MMA and the query rows
 // as its N columns (N = 16 .. 128 as the call needs, so a single new token
 // does not pay for 128 rows).  Per tile of 128 tokens and one KV head:
-//   1. keys: codes -> t = 2q (f16 integers, exact); X = t H on the tensor
+//   1. keys: codes -> t = 2q, q the lattice point (f16 integers, exact); X = t H on the tensor
 //      cores: with H128 = [[H64, H64], [H64, -H64]] the two halves u = H64 t_lo
 //      and v = H64 t_hi take half the products, and the last butterfly costs
 //      nothing inside the rotation:
@@ -31,14 +31,21 @@
 // One CTA per SM, its warpgroups specialised so that the phases of different
 // tiles overlap: two or four warpgroups make keys (a token per thread and a
 // part of its coordinates: codes -> t, then X -> rotated keys), one makes
-// values, two do the softmax (half of the query rows each), and the last
-// one's warps issue the three products.  X is double buffered in TMEM, so the
-// codes of tile j+1 go to the tensor cores before tile j is rotated.
-// Registers are moved to the softmax warpgroups, which hold a sum per query
-// row.  The work of a
-// launch is split over the tokens (flash decoding) to fill the 148 SMs;
-// tree_combine_kernel merges the splits, applies H and attends the draft
-// nodes in fp32.
+// values, two or four do the softmax (a part of the query rows each), and the
+// last one's warps issue the three products.  X is double buffered in TMEM (up
+// to 64 columns), so the codes of tile j+1 go to the tensor cores before tile j
+// is rotated.  Registers are moved to the softmax warpgroups, which hold a sum
+// per query row.  The work of a launch is split over the tokens (flash
+// decoding) to fill the 148 SMs; tree_combine_kernel merges the splits, applies
+// H and attends the draft nodes in fp32.
+//
+// What bounds it: the instructions of the warps that unpack and rotate (a
+// 64-column call issues in 68 % of the cycles, a third of that in waits; tensor
+// pipe 20 %, DRAM below 10 %).  Per call with 8 KV heads, 3-bit keys and 2-bit
+// values: 32 units x 13 147 tokens, one node of 4 heads (16 columns), 350 us
+// against 45 us for the bytes alone (296 MB at 6567 GB/s); a tree of 64 nodes x
+// 4 heads over 131 072 tokens, 395 us = 347 TFLOP/s of the attention's own
+// 4 R n 128 operations per KV head.
 //
 // The angles of a tile are needed by every KV head and every row block:
 // tree_angles_kernel writes (c', s') once per call as f16 pairs in the order
@@ -84,7 +91,8 @@ __device__ __forceinline__ int64_t tree_len(const TreeLaunch& L, int64_t u) {
 // entry e (16 bytes) holds frequencies 4e .. 4e+3 as (c' pair, s' pair, c'
 // pair, s' pair), the 128 tokens of a tile side by side.  A warp reads each
 // token's two table rows whole (lane l: frequencies 2l, 2l+1) and the tile
-// goes through shared memory, so that both sides are contiguous.
+// goes through shared memory, so that both sides are contiguous.  32 lists
+// of 13 147 positions, 108 MB written: 36 us, 3.0 TB/s.
 constexpr int kAngleThreads = 256;
 constexpr int kAnglePitch = 256 + 16;  // bytes per token: neither side has bank conflicts
 __global__ void __launch_bounds__(kAngleThreads) tree_angles_kernel(const TreeArgs a) {
@@ -333,7 +341,8 @@ __device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // A 128-byte swizzled operand whose first row is at 16 * addr4, groups of 8
-// rows 1024 bytes apart (see desc_sw128, desc_sw128_mn).
+// rows 1024 bytes apart: K-major (see desc_sw128), or MN-major, a row of 128
+// bytes (64 elements along M or N) per k, the next 64 elements 16 * lbo4 bytes on.
 __device__ __forceinline__ uint64_t tree_desc(uint32_t addr4, uint32_t lbo4) {
   constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
   return (static_cast<uint64_t>(kHigh) << 32) | (addr4 | (lbo4 << 16));
@@ -745,7 +754,8 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
     // Thread (t, w): token t, query rows HN w .. HN w + HN - 1 of the block.
     setup_done();
     set_regs<R::Launch, R::Softmax>();
-    constexpr int HN = N / R::SW, CH = HN < 32 ? HN : 32;  // columns; columns at a time
+    constexpr int HN = N / R::SW;
+    static_assert(HN <= 32, "a warp's lanes hold a column each");
     const int w = (warp - R::Softmax0) >> 2, wl = warp & 3;
     const uint32_t bid = 1 + w;  // this warpgroup's named barrier
     float4* fm = reinterpret_cast<float4*>(gen + S::FM) + w * (HN / 2);
@@ -762,140 +772,135 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
       const bool valid = kv >= 0.f;
       const float vm = reinterpret_cast<const float*>(gen + S::Vm)[(j & 7) * 128 + t];
       bool raised = false;
+      float y[HN];
+      {
+        constexpr int LD = HN < 16 ? HN : 16;
 #pragma unroll
-      for (int h0 = 0; h0 < HN; h0 += CH) {
-        float y[CH];
-        {
-          constexpr int LD = CH < 16 ? CH : 16;
+        for (int c0 = 0; c0 < HN; c0 += LD) {
+          uint32_t s[LD];
+          tmem_ld(tS + t_lane + w * HN + c0, s);
+          tmem_wait_ld(s);
 #pragma unroll
-          for (int c0 = 0; c0 < CH; c0 += LD) {
-            uint32_t s[LD];
-            tmem_ld(tS + t_lane + w * HN + h0 + c0, s);
-            tmem_wait_ld(s);
+          for (int c = 0; c < LD; c += 2) {
+            const float4 f = fm[(c0 + c) / 2];
+            const float2 g = mul2(make_float2(f.x, f.y), make_float2(kv, kv));
+            const float2 v = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                                  g, make_float2(f.z, f.w));
+            y[c0 + c] = v.x;
+            y[c0 + c + 1] = v.y;
+          }
+        }
+      }
+      tc_fence_before();  // S has been read
+      warp_arrive(bar_sf, lane);
+      if (!valid) {
 #pragma unroll
-            for (int c = 0; c < LD; c += 2) {
-              const float4 f = fm[(h0 + c0 + c) / 2];
-              const float2 g = mul2(make_float2(f.x, f.y), make_float2(kv, kv));
-              const float2 v = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
-                                    g, make_float2(f.z, f.w));
-              y[c0 + c] = v.x;
-              y[c0 + c + 1] = v.y;
+        for (int c = 0; c < HN; ++c) y[c] = -INFINITY;
+      }
+      float top = y[0];
+#pragma unroll
+      for (int c = 1; c < HN; ++c) top = fmaxf(top, y[c]);
+      const bool raise = named_bar_or(bid, 128, top > kTreeTop || (!started && valid));
+      if (j > 1)  // the weights of tile j-2 have been read
+        tree_wait(bar_o(j), ((j >> 1) - 1) & 1, dead);
+      if (raise && !started) {
+        // the first tokens of the split: every column's exact maximum (lane c
+        // of a warp: column c), before which the references are 0
+        raised = true;
+        float x[HN];
+#pragma unroll
+        for (int c = 0; c < HN; ++c) x[c] = y[c];
+        const float k = column_reduce<HN>(x, lane, [](float p, float q) { return fmaxf(p, q); });
+        float* fmax4 = reinterpret_cast<float*>(wmax);
+        if (lane < HN) fmax4[lane * 4 + wl] = k;
+        named_bar_sync(bid, 128);
+        if (wl == 0 && lane < HN) {
+          const float4 k4 = *reinterpret_cast<const float4*>(fmax4 + lane * 4);
+          float* m = reinterpret_cast<float*>(fm + (lane >> 1)) + 2 + (lane & 1);
+          *m = kTreeStart - fmaxf(fmaxf(k4.x, k4.y), fmaxf(k4.z, k4.w));
+        }
+        named_bar_sync(bid, 128);  // the references are written, wmax is free
+#pragma unroll
+        for (int c = 0; c < HN; c += 2) {
+          const float4 f = fm[c / 2];
+          y[c] += f.z;
+          y[c + 1] += f.w;
+        }
+      } else if (raise) {
+        // the sums are to be rescaled: O at rest (the wait above keeps this
+        // barrier from being a phase further)
+        if (j > 0) tree_wait(bar_o(j - 1), ((j - 1) >> 1) & 1, dead);
+        tc_fence_after();
+        raised = true;
+        // the columns to move: those past the range
+        uint32_t cols = 0u;
+#pragma unroll
+        for (int c = 0; c < HN; ++c)
+          if (y[c] > kTreeTop) cols |= 1u << c;
+        cols = __reduce_or_sync(0xffffffffu, cols);
+        uint32_t* wor = reinterpret_cast<uint32_t*>(gen + S::WOr) + w * 4;
+        if (lane == 0) wor[wl] = cols;
+        named_bar_sync(bid, 128);
+        const uint4 o4 = *reinterpret_cast<const uint4*>(wor);
+        cols = (o4.x | o4.y) | (o4.z | o4.w);
+        // their exact maxima over the tile, as ordered integers
+#pragma unroll
+        for (int c = 0; c < HN; ++c)
+          if (cols >> c & 1u) {
+            const int i = __float_as_int(y[c]);
+            const int k = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
+            if (lane == 0) wmax[c * 4 + wl] = k;
+          }
+        named_bar_sync(bid, 128);
+        auto delta_of = [&](int c) {
+          const int4 k4 = *reinterpret_cast<const int4*>(wmax + c * 4);
+          const int k = max(max(k4.x, k4.y), max(k4.z, k4.w));
+          return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)) - kTreeStart;
+        };
+        if (t < HN && (cols >> t & 1u)) {
+          float* m = reinterpret_cast<float*>(fm + (t >> 1)) + 2 + (t & 1);
+          *m -= delta_of(t);
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < HN; c0 += 4) {
+          if ((cols >> c0 & 15u) == 0u) continue;
+          float al[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            al[c] = 1.0f;
+            if (cols >> (c0 + c) & 1u) {
+              const float d = delta_of(c0 + c);
+              y[c0 + c] -= d;
+              al[c] = ex2(-d);
+              l[c0 + c] *= al[c];
             }
           }
+          uint32_t o[4];
+          tmem_ld(tO + t_lane + w * HN + c0, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
+          tmem_st(tO + t_lane + w * HN + c0, o);
         }
-        if (h0 + CH == HN) {  // S has been read
-          tc_fence_before();
-          warp_arrive(bar_sf, lane);
-        }
-        if (!valid) {
+        tmem_wait_st();
+        named_bar_sync(bid, 128);  // the references are written, wmax is free
+      }
+      uint32_t pk[HN / 2];
 #pragma unroll
-          for (int c = 0; c < CH; ++c) y[c] = -INFINITY;
-        }
-        float top = y[0];
+      for (int c = 0; c < HN; c += 2) {
+        const float2 p = make_float2(ex2(y[c]), ex2(y[c + 1]));
+        const float2 s2 = add2(make_float2(l[c], l[c + 1]), p);
+        l[c] = s2.x;
+        l[c + 1] = s2.y;
+        const float2 pm = mul2(p, make_float2(vm, vm));
+        const __half2 ph = __floats2half2_rn(pm.x, pm.y);
+        pk[c / 2] = *reinterpret_cast<const uint32_t*>(&ph);
+      }
 #pragma unroll
-        for (int c = 1; c < CH; ++c) top = fmaxf(top, y[c]);
-        const bool raise = named_bar_or(bid, 128, top > kTreeTop || (!started && valid));
-        if (h0 == 0 && j > 1)  // the weights of tile j-2 have been read
-          tree_wait(bar_o(j), ((j >> 1) - 1) & 1, dead);
-        if (raise && !started) {
-          // the first tokens of the split: every column's exact maximum (lane c
-          // of a warp: column h0 + c), before which the references are 0
-          raised = true;
-          float x[CH];
-#pragma unroll
-          for (int c = 0; c < CH; ++c) x[c] = y[c];
-          const float k = column_reduce<CH>(x, lane, [](float p, float q) { return fmaxf(p, q); });
-          float* fmax4 = reinterpret_cast<float*>(wmax);
-          if (lane < CH) fmax4[(h0 + lane) * 4 + wl] = k;
-          named_bar_sync(bid, 128);
-          if (wl == 0 && lane < CH) {
-            const float4 k4 = *reinterpret_cast<const float4*>(fmax4 + (h0 + lane) * 4);
-            float* m = reinterpret_cast<float*>(fm + ((h0 + lane) >> 1)) + 2 + (lane & 1);
-            *m = kTreeStart - fmaxf(fmaxf(k4.x, k4.y), fmaxf(k4.z, k4.w));
-          }
-          named_bar_sync(bid, 128);  // the references are written, wmax is free
-#pragma unroll
-          for (int c = 0; c < CH; c += 2) {
-            const float4 f = fm[(h0 + c) / 2];
-            y[c] += f.z;
-            y[c + 1] += f.w;
-          }
-        } else if (raise) {
-          // the sums are to be rescaled: O at rest (the wait above keeps this
-          // barrier from being a phase further)
-          if (j > 0) tree_wait(bar_o(j - 1), ((j - 1) >> 1) & 1, dead);
-          tc_fence_after();
-          raised = true;
-          // the columns to move: those past the range
-          uint32_t cols = 0u;
-#pragma unroll
-          for (int c = 0; c < CH; ++c)
-            if (y[c] > kTreeTop) cols |= 1u << c;
-          cols = __reduce_or_sync(0xffffffffu, cols);
-          uint32_t* wor = reinterpret_cast<uint32_t*>(gen + S::WOr) + w * 4;
-          if (lane == 0) wor[wl] = cols;
-          named_bar_sync(bid, 128);
-          const uint4 o4 = *reinterpret_cast<const uint4*>(wor);
-          cols = (o4.x | o4.y) | (o4.z | o4.w);
-          // their exact maxima over the tile, as ordered integers
-#pragma unroll
-          for (int c = 0; c < CH; ++c)
-            if (cols >> c & 1u) {
-              const int i = __float_as_int(y[c]);
-              const int k = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));
-              if (lane == 0) wmax[(h0 + c) * 4 + wl] = k;
-            }
-          named_bar_sync(bid, 128);
-          auto delta_of = [&](int c) {
-            const int4 k4 = *reinterpret_cast<const int4*>(wmax + c * 4);
-            const int k = max(max(k4.x, k4.y), max(k4.z, k4.w));
-            return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)) - kTreeStart;
-          };
-          if (t < CH && (cols >> t & 1u)) {
-            float* m = reinterpret_cast<float*>(fm + ((h0 + t) >> 1)) + 2 + (t & 1);
-            *m -= delta_of(h0 + t);
-          }
-#pragma unroll
-          for (int c0 = 0; c0 < CH; c0 += 4) {
-            if ((cols >> c0 & 15u) == 0u) continue;
-            float al[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              al[c] = 1.0f;
-              if (cols >> (c0 + c) & 1u) {
-                const float d = delta_of(h0 + c0 + c);
-                y[c0 + c] -= d;
-                al[c] = ex2(-d);
-                l[h0 + c0 + c] *= al[c];
-              }
-            }
-            uint32_t o[4];
-            tmem_ld(tO + t_lane + w * HN + h0 + c0, o);
-            tmem_wait_ld(o);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * al[c]);
-            tmem_st(tO + t_lane + w * HN + h0 + c0, o);
-          }
-          tmem_wait_st();
-          named_bar_sync(bid, 128);  // the references are written, wmax is free
-        }
-        uint32_t pk[CH / 2];
-#pragma unroll
-        for (int c = 0; c < CH; c += 2) {
-          const float2 p = make_float2(ex2(y[c]), ex2(y[c + 1]));
-          const float2 s2 = add2(make_float2(l[h0 + c], l[h0 + c + 1]), p);
-          l[h0 + c] = s2.x;
-          l[h0 + c + 1] = s2.y;
-          const float2 pm = mul2(p, make_float2(vm, vm));
-          const __half2 ph = __floats2half2_rn(pm.x, pm.y);
-          pk[c / 2] = *reinterpret_cast<const uint32_t*>(&ph);
-        }
-#pragma unroll
-        for (int c = 0; c < CH; c += 8) {
-          const int col = w * HN + h0 + c;
-          sts128(base + S::P + (j & 1) * S::PBytes + (col / 64) * 16384 + row_chunk(t, (col % 64) >> 3),
-                 make_uint4(pk[c / 2], pk[c / 2 + 1], pk[c / 2 + 2], pk[c / 2 + 3]));
-        }
+      for (int c = 0; c < HN; c += 8) {
+        const int col = w * HN + c;
+        sts128(base + S::P + (j & 1) * S::PBytes + (col / 64) * 16384 + row_chunk(t, (col % 64) >> 3),
+               make_uint4(pk[c / 2], pk[c / 2 + 1], pk[c / 2 + 2], pk[c / 2 + 3]));
       }
       started = started || raised;
       fence_proxy_async_smem();
@@ -908,7 +913,7 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
     // ---- the split's sums: lane = code coordinate of this thread's TMEM lane
     const int coord = 32 * (t >> 5) + tree_slot<BV>(t & 31);
     float* out = part + w * HN * part_row + 2 + coord;
-    const int left = a.rows - row0 - w * HN;  // rows of this half that exist
+    const int left = a.rows - row0 - w * HN;  // rows of this warpgroup's that exist
 #pragma unroll
     for (int c0 = 0; c0 < HN; c0 += 8) {
       uint32_t o[8];
@@ -921,14 +926,8 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
       }
     }
     float* wsum = reinterpret_cast<float*>(wmax);
-#pragma unroll
-    for (int c0 = 0; c0 < HN; c0 += CH) {
-      float x[CH];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) x[c] = l[c0 + c];
-      const float k = column_reduce<CH>(x, lane, [](float p, float q) { return p + q; });
-      if (lane < CH) wsum[(c0 + lane) * 4 + wl] = k;
-    }
+    const float k = column_reduce<HN>(l, lane, [](float p, float q) { return p + q; });
+    if (lane < HN) wsum[lane * 4 + wl] = k;
     named_bar_sync(bid, 128);
     if (t < HN && row0 + w * HN + t < a.rows) {
       const float4 s = *reinterpret_cast<const float4*>(wsum + t * 4);
@@ -1019,7 +1018,8 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
 // One warp per row: merge the splits, apply H, attend the draft nodes that
 // the row sees (fp32).  Lane l owns coordinates l, l+32, l+64, l+96; a draft
 // score takes eight lanes (16 coordinates each).  Latency counts here: the
-// loads of a phase are independent of each other.
+// loads of a phase are independent of each other.  8 to 22 us in the calls
+// above, a launch of latency in the shortest ones.
 constexpr int kCombineWarps = 4;
 
 __device__ __forceinline__ float warp_max(float v) {

@@ -401,9 +401,9 @@ nq_status nq_e8_box_quantise(const float *y, int64_t groups, int bits, uint32_t 
  * The call changes none of lens, free_pages and *taken: repeated on the same
  * values it gives the same tables.  slots, positions, lens_out, starts
  * (int32 [requests + 1]) and used (int32 [2]) must not overlap lens, counts,
- * free_pages, *taken or table.  1 <= requests <= 8192, 1 <= page_size <= 65536,
+ * free_pages, *taken or table.  0 <= requests <= 8192, 1 <= page_size <= 65536,
  * 1 <= table_stride <= 2^24 (above: NQ_ERR_UNSUPPORTED); n_free >= 0,
- * 0 <= max_rows < 2^31.  requests = 0 writes the rows and used only. */
+ * 0 <= max_rows < 2^31.  requests = 0 writes starts, the rows and used only. */
 #define NQ_PAGE_TABLES_MAX_REQUESTS 8192
 nq_status nq_page_tables(const int32_t *lens, const int32_t *counts, int requests, int page_size,
                          const int32_t *free_pages, int64_t n_free, const int32_t *taken,
@@ -480,8 +480,10 @@ nq_status nq_encode_slots(const void *K, nq_kv_strides ks, const void *V, nq_kv_
  * (strides os; must not overlap the inputs).  The packed part runs on the
  * tensor cores with f16 operands and fp32 accumulators: keys are rounded to
  * f16 after the rotation (2^-12 relative, as are the cos/sin), queries are
- * scaled by a power of two per row (exact), softmax weights are rounded to
- * f16 (codes are exact), and statistics, sums and the draft part are fp32.
+ * scaled by a power of two per row (exact), softmax weights, times the
+ * mantissa of their value's scale, are rounded to f16 (the value's codes times
+ * the power of two left are exact), and statistics, sums and the draft part
+ * are fp32.
  * Queries must be finite, of a largest |q| per row in [2^-100, 2^100] or 0,
  * and draft keys and values that some node sees finite.
  * Scores beyond 2^15 (in log2 units) are out of range of the fp32 exponent

@@ -44,7 +44,7 @@
 // pipe 20 %, DRAM below 10 %).  Per call with 8 KV heads, 3-bit keys and 2-bit
 // values: 32 units x 13 147 tokens, one node of 4 heads (16 columns), 350 us
 // against 45 us for the bytes alone (296 MB at 6567 GB/s); a tree of 64 nodes x
-// 4 heads over 131 072 tokens, 395 us = 347 TFLOP/s of the attention's own
+// 4 heads over 131 072 tokens, 345 us = 398 TFLOP/s of the attention's own
 // 4 R n 128 operations per KV head.
 //
 // The angles of a tile are needed by every KV head and every row block:
@@ -366,16 +366,23 @@ __device__ __forceinline__ void regs_dec() {
 // Warpgroups of the roles (KW: threads that share a token's key, SW: that
 // share its scores) and their registers per thread, out of Launch x threads
 // that the block starts with.  Up to 64 columns the key warpgroups bound the
-// pipeline, so they are four; with 128 the softmax would, and gets four.
+// pipeline, so they are four; with 128 the softmax would, and gets four.  The
+// split with 128 columns: 64 registers for the keys and 80 for the softmax take
+// 353 us on 64 nodes x 4 heads over 131 072 tokens, 48 and 88 take 392, 64 and
+// 72 take 368.  With 64 columns 56 and 96 take 344 us on 32 ragged units of up
+// to 16 384 tokens, 64 and 88 take 361.
 template <int N>
 struct TreeRoles {
   static constexpr int KW = N > 64 ? 2 : 4, SW = N > 64 ? 4 : 2;
   static constexpr int Values0 = 4 * KW, Softmax0 = Values0 + 4, Issue0 = Softmax0 + 4 * SW;  // warps
   static constexpr int Threads = 32 * (Issue0 + 4), Launch = 64;
   static_assert(Threads == 1024, "eight warpgroups");
-  static constexpr int Softmax = N > 64 ? 88 : (N > 32 ? 96 : 64), Keys = N > 64 ? 48 : (N > 32 ? 56 : 64),
+  static constexpr int Softmax = N > 64 ? 80 : (N > 32 ? 96 : 64), Keys = N > 64 ? 64 : (N > 32 ? 56 : 64),
                        Values = N > 64 ? 40 : (N > 32 ? 56 : 64), Issue = N > 64 ? 24 : (N > 32 ? 32 : 64);
   static_assert(SW * Softmax + KW * Keys + Values + Issue <= 8 * Launch, "the launch's registers");
+  // only the softmax takes more than it was launched with, and only after the
+  // setup's barrier, behind which the others wait for nothing before they give
+  static_assert(Keys <= Launch && Values <= Launch && Issue <= Launch, "no wait for registers before the barrier");
 };
 template <int LAUNCH, int WANT>
 __device__ __forceinline__ void set_regs() {
@@ -655,17 +662,25 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
       tc_fence_after();
       const uint32_t kb = S::tK + t_lane + (j % S::KBufs) * 64 + 4 * NQ * kw;
       const uint32_t x0 = S::tX + t_lane + (j % S::XBufs) * 128 + 8 * NQ * kw;
-      uint32_t uu[2][8], vv[2][8];
+      // (a key thread of 128 columns has no registers for a second buffer: with
+      // one it takes 402 us where one buffer takes 353)
+      constexpr int XB = N > 64 ? 1 : 2;
+      uint32_t uu[XB][8], vv[XB][8];
       tmem_ld(x0, uu[0]);
       tmem_ld(x0 + 64, vv[0]);
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {  // eight frequencies at a time
-        tmem_wait_ld(uu[q & 1]);
-        tmem_wait_ld(vv[q & 1]);
-        if (q + 1 < NQ) {
-          tmem_ld(x0 + 8 * (q + 1), uu[(q + 1) & 1]);
-          tmem_ld(x0 + 64 + 8 * (q + 1), vv[(q + 1) & 1]);
-        } else if (S::XBufs == 1) {  // X has been read
+        if (XB == 1 && q > 0) {
+          tmem_ld(x0 + 8 * q, uu[0]);
+          tmem_ld(x0 + 64 + 8 * q, vv[0]);
+        }
+        tmem_wait_ld(uu[q % XB]);
+        tmem_wait_ld(vv[q % XB]);
+        if (XB == 2 && q + 1 < NQ) {
+          tmem_ld(x0 + 8 * (q + 1), uu[(q + 1) % XB]);
+          tmem_ld(x0 + 64 + 8 * (q + 1), vv[(q + 1) % XB]);
+        }
+        if (S::XBufs == 1 && q + 1 == NQ) {  // X has been read
           tc_fence_before();
           warp_arrive(bar_xf, lane);
         }
@@ -677,10 +692,10 @@ __global__ void __launch_bounds__(TreeRoles<N>::Threads, 1) tree_partial_kernel(
           const __half2 c = *reinterpret_cast<const __half2*>(&cw);
           const __half2 s = *reinterpret_cast<const __half2*>(&sw);
           // u and v are integers up to 448: exact in f16
-          const __half2 U = __floats2half2_rn(__uint_as_float(uu[q & 1][2 * f]),
-                                              __uint_as_float(uu[q & 1][2 * f + 1]));
-          const __half2 V = __floats2half2_rn(__uint_as_float(vv[q & 1][2 * f]),
-                                              __uint_as_float(vv[q & 1][2 * f + 1]));
+          const __half2 U = __floats2half2_rn(__uint_as_float(uu[q % XB][2 * f]),
+                                              __uint_as_float(uu[q % XB][2 * f + 1]));
+          const __half2 V = __floats2half2_rn(__uint_as_float(vv[q % XB][2 * f]),
+                                              __uint_as_float(vv[q % XB][2 * f + 1]));
           const __half2 a0 = __hfma2(U, c, __hmul2(V, s));
           const __half2 a1 = __hfma2(__hneg2(V), c, __hmul2(U, s));
           lo[f] = *reinterpret_cast<const uint32_t*>(&a0);
@@ -1180,7 +1195,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tree_combine_kernel(const 
 }
 
 // ------------------------------------------------------------------ launch
-constexpr int kTreeTileCost[4] = {31, 33, 41, 69};
+constexpr int kTreeTileCost[4] = {31, 33, 41, 59};
 
 struct TreePlan {
   int cols, rblocks;
@@ -1188,10 +1203,11 @@ struct TreePlan {
 };
 
 // Rows per CTA (columns of the products): the width whose blocks take the
-// least time together.  A tile takes 31, 33, 41 and 69 units with 16, 32, 64
-// and 128 columns (measured on 32 x 8 x 13 147 tokens: 306, 330, 405, 690 us of
+// least time together.  A tile takes 31, 33, 41 and 59 units with 16, 32, 64
+// and 128 columns (measured on 32 x 8 x 13 147 tokens: 306, 330, 405, 592 us of
 // this kernel; below 64 columns the keys are the work), so two blocks of 64
-// lose to one of 128, and three beat two of 128.
+// lose to one of 128, and three to two (160 rows on that shape: 1255 against
+// 1125 us per call).
 // Splits: the launch costs (waves of 148 CTAs) * (tiles per CTA + setup, about
 // three tiles); the smallest cost, the fewest splits among equals.  Units that
 // may hold fewer than n tokens (their lengths are on the device) even out only

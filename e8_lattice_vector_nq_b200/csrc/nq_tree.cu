@@ -44,7 +44,7 @@
 // pipe 20 %, DRAM below 10 %).  Per call with 8 KV heads, 3-bit keys and 2-bit
 // values: 32 units x 13 147 tokens, one node of 4 heads (16 columns), 350 us
 // against 45 us for the bytes alone (296 MB at 6567 GB/s); a tree of 64 nodes x
-// 4 heads over 131 072 tokens, 345 us = 398 TFLOP/s of the attention's own
+// 4 heads over 131 072 tokens, 340 to 360 us, 380 to 400 TFLOP/s of the attention's own
 // 4 R n 128 operations per KV head.
 //
 // The angles of a tile are needed by every KV head and every row block:

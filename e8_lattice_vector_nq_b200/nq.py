@@ -612,9 +612,10 @@ def _packed(s: PackedStore) -> Packed:
 
 
 def _rope_table(t: torch.Tensor, max_pos: int) -> None:
-    """Tables of rope_tables() for at least max_pos positions (a shorter one
-    would be read past its end): rows of 64 (cos, sin) pairs."""
-    if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() < ((max_pos + 255) // 256 + 256) * D:
+    """Tables of rope_tables() for max_pos positions: rows of 64 (cos, sin)
+    pairs, the 256 fine ones behind the ceil(max_pos / 256) coarse ones (a
+    shorter table would be read past its end, a longer one at the wrong rows)."""
+    if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != ((max_pos + 255) // 256 + 256) * D:
         raise ValueError(f"rope_tab is not the float32 table of {max_pos} positions")
 
 

@@ -888,3 +888,20 @@ def test_speculative_steps_over_a_paged_store(nq, captured):
                     assert torch.equal(a.codes[pg, :, off].transpose(0, 1), b.codes[0])
                     assert torch.equal(a.meta[pg, :, off].transpose(0, 1), b.meta[0])
     assert nq.device_error() == 0
+
+
+def test_calls_refuse_longer_angle_tables(nq):
+    """A store's table covers its rounded-up length: named with a smaller one
+    it is refused by every call, not read at the wrong rows."""
+    store = nq.PagedStore(1, 1, 4, 3, 100, 250, 1e4)
+    assert store.n == 300
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q, K = z(1, 8, 5, D), z(1, 4, 5, D)
+    for most in (250, 256):
+        with pytest.raises(ValueError):
+            nq.nq_qk_norm_rope(q, K, store.rope, most)
+        with pytest.raises(ValueError):
+            nq.nq_encode_slots(K[0], K[0], *store.layer(0), i32([0] * 5), i32([1] * 5), store.rope, most)
+        with pytest.raises(ValueError):
+            nq.nq_tree_attend(q, K, K, *store.layer(0), 250, store.rope, most, table=store.table)
+    nq.nq_qk_norm_rope(q, K, store.rope, 300)

@@ -173,3 +173,22 @@ def test_binding_refuses_host_tensors(nq):
     for name, call in calls.items():
         with pytest.raises(ValueError, match="no CPU path"):
             call()
+
+
+@pytest.mark.parametrize("built,named", [(131072, 1000), (300, 250), (257, 256), (512, 1), (256, 257)])
+def test_binding_refuses_angle_tables_of_another_length(nq, built, named):
+    """The fine rows follow the coarse ones at row ceil(max_pos / 256), so a
+    table of more positions than the call names is read at the wrong rows just
+    as a shorter one is read past its end."""
+    tab = nq.rope_tables(1e4, built, "cpu")
+    nq._rope_table(tab, built)
+    with pytest.raises(ValueError, match="table"):
+        nq._rope_table(tab, named)
+
+
+def test_binding_takes_tables_of_the_same_rows(nq):
+    """Lengths that round up to the same number of coarse rows share a table."""
+    tab = nq.rope_tables(1e4, 300, "cpu")
+    assert torch.equal(tab, nq.rope_tables(1e4, 512, "cpu"))
+    for named in (257, 300, 512):
+        nq._rope_table(tab, named)

@@ -603,12 +603,18 @@ def _contiguous4(t: torch.Tensor) -> KVStrides:
 
 
 def _packed(s: PackedStore) -> Packed:
-    """PackedStore.desc with one check."""
-    u, h, _ = s.meta.stride()
+    """PackedStore.desc with its layout checked: units and heads anywhere, the
+    slots of a head side by side."""
+    c, m = s.codes, s.meta
+    u, h, t = m.stride()
     w = 4 * s.bits
-    if s.codes.stride()[:2] != (u * w, h * w):
-        raise ValueError("codes and meta of a store must be laid out alike")
-    return Packed(s.codes.data_ptr(), s.meta.data_ptr(), u, h, s.bits)
+    cs = c.stride()
+    if c.dtype != torch.int32 or m.dtype != torch.int32 or c.get_device() != m.get_device():
+        raise ValueError("codes and meta of a store must be int32 tensors of one device")
+    if c.shape != (*m.shape, w) or cs[:2] != (u * w, h * w) or cs[3] != 1 or \
+            (m.shape[2] > 1 and (cs[2] != w or t != 1)):
+        raise ValueError("codes and meta of a store must be laid out alike, slots side by side")
+    return Packed(c.data_ptr(), m.data_ptr(), u, h, s.bits)
 
 
 def _rope_table(t: torch.Tensor, max_pos: int) -> None:

@@ -905,3 +905,18 @@ def test_calls_refuse_longer_angle_tables(nq):
         with pytest.raises(ValueError):
             nq.nq_tree_attend(q, K, K, *store.layer(0), 250, store.rope, most, table=store.table)
     nq.nq_qk_norm_rope(q, K, store.rope, 300)
+
+
+def test_calls_refuse_strided_slots(nq):
+    """Every other slot of a store, which the kernels would read (and write) as
+    neighbours."""
+    ks, vs = nq.PackedStore.empty(2, 4, 64, 3), nq.PackedStore.empty(2, 4, 64, 2)
+    thin = lambda s: nq.PackedStore(s.codes[:, :, ::2], s.meta[:, :, ::2], s.bits)  # noqa: E731
+    tab = nq.rope_tables(1e4, 64)
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q, K = z(2, 8, 5, D), z(2, 4, 5, D)
+    for k, v in ((thin(ks), thin(vs)), (thin(ks), nq.PackedStore.empty(2, 4, 32, 2))):
+        with pytest.raises(ValueError):
+            nq.nq_tree_attend(q, K, K, k, v, 20, tab, 64)
+        with pytest.raises(ValueError):
+            nq.nq_encode_slots(K[0], K[0], k, v, i32([0] * 5), i32([1] * 5), tab, 64)

@@ -192,3 +192,23 @@ def test_binding_takes_tables_of_the_same_rows(nq):
     assert torch.equal(tab, nq.rope_tables(1e4, 512, "cpu"))
     for named in (257, 300, 512):
         nq._rope_table(tab, named)
+
+
+def test_binding_refuses_stores_laid_out_otherwise(nq):
+    """The kernels take two strides per store and find slots side by side:
+    strided slots, codes of other slots than meta's, of another type or of
+    another width are refused, views that keep the layout are not."""
+    ok = nq.PackedStore.empty(4, 8, 16, 3, "cpu")
+    c, m = ok.codes, ok.meta
+    for st in (ok, ok.select_units(slice(1, 4, 2)), nq.PackedStore(c[:, 2:5], m[:, 2:5], 3),
+               nq.PackedStore(c[:, :, 5:9], m[:, :, 5:9], 3), nq.PackedStore.empty(4, 8, 1, 3, "cpu")):
+        d = nq._packed(st)
+        assert (d.codes, d.meta) == (st.codes.data_ptr(), st.meta.data_ptr())
+        assert (d.unit_stride, d.head_stride, d.bits) == (*st.meta.stride()[:2], 3)
+    other = torch.empty(4, 8, 16, 24, dtype=torch.int32)[..., ::2]
+    for codes, meta, bits in ((c[:, :, ::2], m[:, :, ::2], 3), (c[:, :, :9], m, 3), (c[:3], m, 3),
+                              (c[:, :5], m, 3), (c, m, 2), (c[..., :8], m, 2), (c, m, 4),
+                              (c.float(), m, 3), (c, m.float(), 3), (other, m, 3),
+                              (c, torch.empty(4, 8, 32, dtype=torch.int32)[:, :, ::2], 3)):
+        with pytest.raises(ValueError):
+            nq._packed(nq.PackedStore(codes, meta, bits))

@@ -1183,10 +1183,11 @@ class PagedStore:
         k, v = self.layer(layer)
         nq_encode_slots(K, V, k, v, slots, positions, self.rope, self.n, stream=stream)
 
-    def commit(self, plan: PageTables):
-        """Take over the lengths and pages of a plan (on the current stream)."""
-        self.lens.copy_(plan.lens)
-        self.taken.copy_(plan.used[:1])
+    def commit(self, plan: PageTables, stream=None):
+        """Take over the lengths and pages of a plan, on the stream that made it."""
+        with _stream_on(self.lens.get_device(), stream)[1]:
+            self.lens.copy_(plan.lens)
+            self.taken.copy_(plan.used[:1])
 
     def attend(self, layer: int, q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
                mask: torch.Tensor | None = None, n: int | None = None, **kw):

@@ -920,3 +920,38 @@ def test_calls_refuse_strided_slots(nq):
             nq.nq_tree_attend(q, K, K, k, v, 20, tab, 64)
         with pytest.raises(ValueError):
             nq.nq_encode_slots(K[0], K[0], k, v, i32([0] * 5), i32([1] * 5), tab, 64)
+
+
+def test_paged_store_on_a_side_stream(nq):
+    """A whole step on a stream that is never made current and that is busy with
+    other work at its start: each call waits for the one before it."""
+    S, H, G, P = 4, 2, 2, 16
+    counts = ([20, 0, 33, 5], [3, 7, 0, 12])
+
+    def steps(stream):
+        g = gen(91)
+        store = nq.PagedStore(S, 1, H, 12, P, 64, 1e4)
+        outs = []
+        for c in counts:
+            x = torch.randn(2, H, sum(c) + 2, D, generator=g, device="cuda").to(torch.bfloat16)
+            q = torch.randn(S, H * G, 3, D, generator=g, device="cuda").to(torch.bfloat16)
+            K, V = (torch.randn(S, H, 3, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+            n = i32(c)
+            a = torch.ones(4096, 4096, dtype=torch.bfloat16, device="cuda")
+            torch.cuda.synchronize()
+            if stream is not None:
+                with torch.cuda.stream(stream):
+                    for _ in range(40):
+                        torch.mm(a, a)
+            plan = store.plan(n, sum(c) + 2, stream=stream)
+            store.write(0, x[0], x[1], plan.slots, plan.positions, stream=stream)
+            store.commit(plan, stream=stream)
+            outs.append(store.attend(0, q, K, V, stream=stream))
+            (torch.cuda.current_stream() if stream is None else stream).synchronize()
+            assert store.lens.tolist() == [sum(z) for z in zip(*counts[:len(outs)])]
+        return outs + [store.table, store.lens, store.taken]
+
+    want = steps(None)
+    got = steps(torch.cuda.Stream())
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert nq.device_error() == 0

@@ -1137,6 +1137,25 @@ class AppendStore:
                   V_out, self.rope, self.cap, stream=stream)
 
 
+def _release_pages(done: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                   taken: torch.Tensor, free: torch.Tensor, page_size: int):
+    """Put the pages that the requests done hold before free[taken], in place of
+    list entries that were handed out, and reset their rows; no sizes come to the
+    host.  free has an entry more than the list.  Table entries past a request's
+    length are of plans that were dropped: their pages were never taken.  taken may
+    count past the list (pages had run out): such entries are -1 in the tables."""
+    pages = free.shape[0] - 1
+    have = (lens + (page_size - 1)) // page_size
+    held = torch.arange(table.shape[1], device=table.device) < have[:, None]
+    back = (held & done[:, None] & (table >= 0)).flatten()
+    rank = back.cumsum(0)
+    top = taken.clamp(0, pages)
+    free.scatter_(0, torch.where(back, top - rank, pages), table.flatten())
+    taken.copy_(top - back.sum())
+    table.masked_fill_(done[:, None], -1)
+    lens.masked_fill_(done, 0)
+
+
 class PagedStore:
     """Packed caches of many requests in shared pages: per layer a K and a V
     store [pages][heads][page_size], one table of pages and one length per
@@ -1146,11 +1165,14 @@ class PagedStore:
         plan = store.plan(accepted_counts, max_rows)         # pages and slots
         store.write(layer, K_rows, V_rows, plan.slots, plan.positions)
         store.commit(plan)                                   # the new lengths
+        store.release(done)                                  # requests that ended
 
     A prompt is the same with its own counts.  Tokens sit at their positions
     (token t of a request at RoPE position t).  plan() changes nothing but
     fresh table entries, so a plan may be dropped and made again (before
-    commit() a server looks at plan.used[1]: pages or rows may have run out)."""
+    commit() a server looks at plan.used[1]: pages or rows may have run out).
+    A plan belongs to the lengths it was made from: one made before another
+    commit() or a release() is not committed after it."""
 
     def __init__(self, requests: int, layers: int, heads: int, pages: int, page_size: int,
                  max_tokens: int, theta: float, bits_k: int = 3, bits_v: int = 2, device="cuda"):
@@ -1165,7 +1187,9 @@ class PagedStore:
         e = lambda *s, fill: torch.full(s, fill, dtype=torch.int32, device=device)  # noqa: E731
         self.table = e(requests, width, fill=-1)
         self.lens, self.taken = e(requests, fill=0), e(1, fill=0)
-        self.free = torch.arange(pages, dtype=torch.int32, device=device)
+        # (one entry more than the list: where release() puts what is no page)
+        self._free = torch.arange(pages + 1, dtype=torch.int32, device=device)
+        self.free = self._free[:pages]
 
     def layer(self, layer: int) -> tuple[PackedStore, PackedStore]:
         sl = slice(layer * self.pages, (layer + 1) * self.pages)
@@ -1188,6 +1212,14 @@ class PagedStore:
         with _stream_on(self.lens.get_device(), stream)[1]:
             self.lens.copy_(plan.lens)
             self.taken.copy_(plan.used[:1])
+
+    def release(self, done: torch.Tensor, stream=None):
+        """End the requests s with done[s] (bool [requests], on the device): their
+        pages go back to the front of the free list, their lengths to 0."""
+        if done.dtype != torch.bool or done.shape != (self.S,) or done.device != self.lens.device:
+            raise ValueError(f"done must be bool [{self.S}] on the store's device")
+        with _stream_on(self.lens.get_device(), stream)[1]:
+            _release_pages(done, self.table, self.lens, self.taken, self._free, self.P)
 
     def attend(self, layer: int, q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
                mask: torch.Tensor | None = None, n: int | None = None, **kw):

@@ -955,3 +955,78 @@ def test_paged_store_on_a_side_stream(nq):
     got = steps(torch.cuda.Stream())
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     assert nq.device_error() == 0
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_paged_store_serves_on_as_requests_end(nq, captured):
+    """Requests come and go for many steps over a pool that holds a few of them:
+    with their pages released nothing runs out, no page is in two rows, and each
+    request's attention is that over its own tokens alone (a store of its own, the
+    same kernel: two outputs rounded to bf16 differ by a step at most, 2^-7
+    relative; two sets of weights rounded to f16 by 2^-10 of sum p |v|, which is
+    below 8 norms of sum p v for 66 keys of independent values, 2^-7 again; a
+    wrong page is off by about the norm itself).  Captured: plan, write, commit, attention and release of a
+    step are one graph, replayed with other counts and endings."""
+    S, H, G, P, pages, rows, T = 3, 2, 2, 16, 14, 96, 64
+    g, rng = gen(93), np.random.default_rng(93)
+    store = nq.PagedStore(S, 1, H, pages, P, T, 1e4)
+    counts, done = i32([0] * S), torch.zeros(S, dtype=torch.bool, device="cuda")
+    x = torch.zeros(2, H, rows, D, dtype=torch.bfloat16, device="cuda")
+    q = torch.randn(S, H * G, 2, D, generator=g, device="cuda").to(torch.bfloat16)
+    K, V = (torch.randn(S, H, 2, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    out, used = torch.zeros_like(q), i32([0, 0])
+
+    def step():
+        plan = store.plan(counts, rows)
+        store.write(0, x[0], x[1], plan.slots, plan.positions)
+        store.commit(plan)
+        used.copy_(plan.used)
+        store.attend(0, q, K, V, out=out)
+        store.release(done)
+
+    graph = None
+    if captured:
+        step()  # (nothing to do: counts and endings are 0)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+    tokens = [[torch.zeros(H, 0, D, dtype=torch.bfloat16, device="cuda")] * 2 for _ in range(S)]
+    total = 0
+    for it in range(12):
+        c = [int(rng.integers(0, min(32, T - t[0].shape[1]) + 1)) for t in tokens]
+        end = rng.random(S) < 0.4
+        total += sum(-(-n // P) for n in c)
+        counts.copy_(i32(c))
+        done.copy_(torch.from_numpy(end))
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+        if captured:
+            graph.replay()
+        else:
+            step()
+        torch.cuda.synchronize()
+        assert used.tolist()[1] == 0
+        at = 0
+        for s in range(S):
+            for i in range(2):
+                tokens[s][i] = torch.cat([tokens[s][i], x[i, :, at:at + c[s]]], 1)
+            at += c[s]
+            n = tokens[s][0].shape[1]
+            ks, vs = nq.PackedStore.empty(1, H, max(n, 1), 3), nq.PackedStore.empty(1, H, max(n, 1), 2)
+            if n:
+                nq.nq_encode(tokens[s][0][None], tokens[s][1][None], ks, vs, n, store.rope, store.n)
+            one = nq.nq_tree_attend(q[s:s + 1], K[s:s + 1], V[s:s + 1], ks, vs, n, store.rope, store.n)
+            assert (out[s:s + 1].float() - one.float()).norm() <= 2.0 ** -6 * one.float().norm()
+            if end[s]:
+                tokens[s] = [t[:, :0] for t in tokens[s]]
+        assert store.lens.tolist() == [t[0].shape[1] for t in tokens]
+        held = [p for s, row in enumerate(store.table.tolist()) for p in row[:-(-tokens[s][0].shape[1] // P)]]
+        rest = store.free[int(store.taken):].tolist()
+        assert sorted(held + rest) == list(range(pages))
+    assert total > 2 * pages and nq.device_error() == 0
+    with pytest.raises(ValueError):
+        store.release(done.int())
+    with pytest.raises(ValueError):
+        store.release(done[:2])
+    with pytest.raises(ValueError):
+        store.release(done.cpu())

@@ -212,3 +212,41 @@ def test_binding_refuses_stores_laid_out_otherwise(nq):
                               (c, torch.empty(4, 8, 32, dtype=torch.int32)[:, :, ::2], 3)):
         with pytest.raises(ValueError):
             nq._packed(nq.PackedStore(codes, meta, bits))
+
+
+@pytest.mark.parametrize("S,P,pages,width", [(1, 1, 3, 4), (5, 16, 40, 9), (7, 3, 11, 6), (64, 64, 300, 12),
+                                             (3, 8, 0, 2)])
+def test_released_pages_return_to_the_list(nq, S, P, pages, width):
+    """Random admissions and endings, a free list that runs out among them: after
+    every release a page is either in one row or in the list, never both, and the
+    rows of the other requests are as they were.  The planning is done here, as
+    nq_page_tables defines it."""
+    import random
+
+    rng = random.Random(S * 1000 + pages)
+    free = torch.arange(pages + 1, dtype=torch.int32)
+    table = torch.full((S, width), -1, dtype=torch.int32)
+    lens, taken = torch.zeros(S, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    ran_out = 0
+    for _ in range(60):
+        new = [rng.randint(0, min(3 * P, width * P - int(x))) if rng.random() < 0.5 else 0 for x in lens]
+        at = int(taken)
+        for s, c in enumerate(new):
+            for j in range(-(-int(lens[s]) // P), -(-(int(lens[s]) + c) // P)):
+                table[s, j] = int(free[at]) if at < pages else -1
+                at += 1
+        if rng.random() < 0.2:  # the plan is dropped: what it wrote stays in the table
+            continue
+        ran_out += at > pages
+        taken.fill_(at)
+        lens += torch.tensor(new, dtype=torch.int32)
+        done = torch.tensor([rng.random() < 0.3 for _ in range(S)])
+        before, held = table.clone(), lens.clone()
+        nq._release_pages(done, table, lens, taken, free, P)
+        assert torch.equal(table[~done], before[~done]) and (table[done] == -1).all()
+        assert torch.equal(lens, torch.where(done, 0, held))
+        rows = [int(table[s, j]) for s in range(S) for j in range(-(-int(lens[s]) // P))]
+        rows = [x for x in rows if x >= 0]
+        assert int(taken) == len(rows)
+        assert sorted(rows + free[int(taken):pages].tolist()) == list(range(pages))
+    assert pages > 0 or ran_out

@@ -13,7 +13,11 @@
 //        o_i = u c' + v s',  o_{i+64} = u s' - v c',  c' = c - s, s' = c + s.
 //      o is rounded to f16 (|o| < 1268: no scale is applied before the product,
 //      so no scale can overflow it) and the key's scale kappa_t multiplies the
-//      score, where a thread has one token and kappa_t is its scalar;
+//      score, where a thread has one token and kappa_t is its scalar.  c', s'
+//      and the rotation are f16 too (two coordinates per instruction): o_i is
+//      off by up to 2^-11 (2 r + |o_i|), r its pair's length; with unit-normal
+//      rows and scale 128^-1/2 that moves a score by 2^-11 sqrt 2 (RMS, at
+//      most), against 2^-8 of an output's rounding to bf16;
 //   2. S^T = o Q^T (fp32 in TMEM), Q scaled per row by a power of two;
 //   3. y = S f_r kappa_t - m_r in log2 units, p = 2^y; the sum over tokens is
 //      kept per thread and reduced once at the end;

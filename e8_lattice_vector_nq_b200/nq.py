@@ -810,7 +810,8 @@ def nq_tree_attend(q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
                    ws: torch.Tensor | None = None, stream=None):
     """Attention of drafted nodes q [units][heads*G][nodes][128] over up to n
     packed tokens per unit and over the nodes' own K_new, V_new
-    [units][heads][nodes][128] (all bf16; see nq.h, nq_tree_attend).
+    [units][heads][nodes][128] (all bf16; see nq.h, nq_tree_attend, also for
+    the rounding of keys and weights to f16: nq_attend is fp32 throughout).
 
     mask: int64 [units][nodes][ceil(nodes/64)] (or [nodes][...], shared), bit m
     of a node's words = it sees node m; None = a chain.  lens: int32 [units]

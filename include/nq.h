@@ -478,12 +478,16 @@ nq_status nq_encode_slots(const void *K, nq_kv_strides ks, const void *V, nq_kv_
  * q: bf16 [units][heads*G][nodes][128] (strides qs); K_new, V_new: bf16
  * [units][heads][nodes][128], already rotated (nq_qk_norm_rope); out like q
  * (strides os; must not overlap the inputs).  The packed part runs on the
- * tensor cores with f16 operands and fp32 accumulators: keys are rounded to
- * f16 after the rotation (2^-12 relative, as are the cos/sin), queries are
- * scaled by a power of two per row (exact), softmax weights, times the
- * mantissa of their value's scale, are rounded to f16 (the value's codes times
- * the power of two left are exact), and statistics, sums and the draft part
- * are fp32.
+ * tensor cores with f16 operands and fp32 accumulators, so it has fewer bits
+ * than nq_attend, which is fp32 throughout.  Keys: cos - sin and cos + sin are
+ * rounded to f16 and the rotation is a rounded f16 product and an f16 fma, so
+ * coordinate i of a key is off by up to 2^-11 (2 r + |k_i|), r the length of
+ * its RoPE pair (no bound relative to |k_i| alone: the pair's parts cancel);
+ * the key's scale is applied to the score in fp32.  Queries are scaled by a
+ * power of two per row (exact).  Softmax weights, times the mantissa of their
+ * value's scale, are rounded to f16: by 2^-11 of themselves, or by 2^-29 of
+ * the row's largest where that is more (the value's codes times the power of
+ * two left are exact).  Statistics, sums and the draft part are fp32.
  * Queries must be finite, of a largest |q| per row in [2^-100, 2^100] or 0,
  * and draft keys and values that some node sees finite.
  * Scores beyond 2^15 (in log2 units) are out of range of the fp32 exponent

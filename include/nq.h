@@ -391,7 +391,7 @@ nq_status nq_e8_box_quantise(const float *y, int64_t groups, int bits, uint32_t 
  *     slots[row] = table[s][t / P] * P + t % P, or -1 where the token has no
  *                 page (an entry below 0, or past the table's row), or where
  *                 that product does not fit 31 bits,
- *     positions[row] = t,
+ *     positions[row] = t (saturated at 2^31 - 1),
  *   rows from starts[requests] to max_rows - 1 (a padded batch): slot -1, position 0;
  *   tokens past max_rows - 1 get no row,
  *   used[0] = c + sum of fresh_s (pages then taken from the front of
@@ -417,7 +417,9 @@ nq_status nq_page_tables(const int32_t *lens, const int32_t *counts, int request
  *   y = x * rsqrt(sum(x^2) / 128 + eps) * w     (w = 1 where the weight is NULL)
  *   o_i = fmaf(y_i, c, -(y_{i+64} s)),  o_{i+64} = fmaf(y_{i+64}, c, y_i s)
  * at pos = pos_base + (positions ? positions[u*pos_stride + t] : t), (c, s)
- * from rope_tab (fp32 throughout, one rounding to the output type).
+ * from rope_tab (fp32 throughout, one rounding to the output type; so is the sum:
+ * a row with |x| above 2^60 may overflow it, which gives 0, and one below 2^-60
+ * may lose it, which matters with an eps below that).
  * q: [units][q_heads][rows][128], k: [units][k_heads][rows][128], each of
  * type in_type with its own strides (in elements of its own type; any order
  * of the dimensions, views of one fused projection included; multiples of 8,

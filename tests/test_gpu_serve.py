@@ -1030,3 +1030,30 @@ def test_paged_store_serves_on_as_requests_end(nq, captured):
         store.release(done[:2])
     with pytest.raises(ValueError):
         store.release(done.cpu())
+
+
+def test_page_tables_lengths_past_31_bits(nq):
+    """A request whose new tokens pass 2^31 - 1: lengths and positions saturate,
+    slots and pages go on."""
+    P, last = 65536, 2 ** 31 - 1
+    table = torch.full((1, 32769), 7, dtype=torch.int32, device="cuda")
+    table[0, 32768] = -1
+    r = nq.nq_page_tables(i32([last - 2]), i32([5]), P, i32([3, 4]), table, 6)
+    assert r.lens.tolist() == [last] and r.starts.tolist() == [0, 5] and r.used.tolist() == [1, 0]
+    assert r.positions.tolist() == [last - 2, last - 1, last, last, last, 0]
+    assert r.slots.tolist() == [8 * P - 3, 8 * P - 2, 8 * P - 1, 3 * P, 3 * P + 1, -1]
+    assert table[0, 32767:].tolist() == [7, 3]
+
+
+@pytest.mark.parametrize("size", [2.0 ** 60, 2.0 ** -60, 1.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_rope_large_and_small_rows(nq, size, dtype):
+    """At the ends of the range that the sum of squares has: 128 * 2^120 and
+    128 * 2^-120 are still normal in fp32."""
+    x = torch.rand(1, 3, 40, D, generator=gen(6), device="cuda") * 2 - 1
+    x[..., 5] = 1.0  # (the largest of a row)
+    x = (x * size).to(dtype)
+    tab, pos = nq.rope_tables(1e4, 40), torch.arange(40, device="cuda")[None]
+    q, _ = nq.nq_qk_norm_rope(x, None, tab, 40, eps=0.0)
+    ref, y = ref_norm(x, None, 0.0, pos, 1e4)
+    assert (q.double() - ref).abs().le(norm_bound(ref, y, dtype)).all()

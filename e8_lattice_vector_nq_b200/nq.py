@@ -602,17 +602,15 @@ def _contiguous4(t: torch.Tensor) -> KVStrides:
     return KVStrides(h * r * d, r * d, d)
 
 
-def _packed(s: PackedStore) -> Packed:
-    """PackedStore.desc with its layout checked: units and heads anywhere, the
-    slots of a head side by side."""
-    c, m = s.codes, s.meta
+def _packed(s: PackedStore, idx: int = -1) -> Packed:
+    """PackedStore.desc of a store on device idx (-1: the host) with its layout
+    checked: units and heads anywhere, the slots of a head side by side."""
+    c, m, w = s.codes, s.meta, 4 * s.bits
     u, h, t = m.stride()
-    w = 4 * s.bits
-    cs = c.stride()
-    if c.dtype != torch.int32 or m.dtype != torch.int32 or c.get_device() != m.get_device():
-        raise ValueError("codes and meta of a store must be int32 tensors of one device")
-    if c.shape != (*m.shape, w) or cs[:2] != (u * w, h * w) or cs[3] != 1 or \
-            (m.shape[2] > 1 and (cs[2] != w or t != 1)):
+    if c.dtype is not torch.int32 or m.dtype is not torch.int32 or c.get_device() != idx or m.get_device() != idx:
+        raise ValueError("codes and meta of a store must be int32 tensors on the tensors' device")
+    if c.shape != (*m.shape, w) or ((c.stride() != (u * w, h * w, w, 1) or t != 1) and (
+            m.shape[2] > 1 or c.stride()[:2] != (u * w, h * w) or c.stride(3) != 1)):
         raise ValueError("codes and meta of a store must be laid out alike, slots side by side")
     return Packed(c.data_ptr(), m.data_ptr(), u, h, s.bits)
 
@@ -777,9 +775,9 @@ def nq_encode_slots(K: torch.Tensor | None, V: torch.Tensor | None, k_out: Packe
         if t.shape != (heads, rows, D) or t.dtype != torch.bfloat16 or t.stride(2) != 1:
             raise ValueError("K and V must be bf16 [heads, rows, 128] alike, the last dimension contiguous")
         shape = shape or s.meta.shape
-        if s.meta.shape != shape or shape[1] != heads or s.meta.get_device() != idx:
-            raise ValueError("the stores must be [pages][heads][page_size] alike, on the tensors' device")
-        desc.append(_packed(s))
+        if s.meta.shape != shape or shape[1] != heads:
+            raise ValueError("the stores must be [pages][heads][page_size] alike")
+        desc.append(_packed(s, idx))
         strides.append(KVStrides(0, t.stride(0) if heads > 1 else 0, t.stride(1) if rows > 1 else 0))
     if rows == 0:  # an empty tensor has no address
         return
@@ -837,8 +835,6 @@ def nq_tree_attend(q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
         lead, h, cap = k_in.meta.shape
         if v_in.meta.shape != (lead, h, cap) or h != heads:
             raise ValueError("k_in and v_in must be [units or pages][heads][slots] alike")
-        if k_in.meta.get_device() != idx or v_in.meta.get_device() != idx:
-            raise ValueError("the stores must be on the queries' device")
         if table is None:
             if lead < units or cap < n:
                 raise ValueError("packed store too small for units x n")
@@ -858,7 +854,7 @@ def nq_tree_attend(q: torch.Tensor, K_new: torch.Tensor, V_new: torch.Tensor,
             ps = _positions(positions, units, n)
             if units > 1 and ps < n:
                 raise ValueError("positions rows overlap")
-        kd, vd = _packed(k_in), _packed(v_in)
+        kd, vd = _packed(k_in, idx), _packed(v_in, idx)
     else:
         table = positions = None
     if lens is not None:

@@ -250,3 +250,11 @@ def test_released_pages_return_to_the_list(nq, S, P, pages, width):
         assert int(taken) == len(rows)
         assert sorted(rows + free[int(taken):pages].tolist()) == list(range(pages))
     assert pages > 0 or ran_out
+
+
+def test_binding_takes_a_store_of_one_slot_with_any_slot_stride(nq):
+    ok = nq.PackedStore.empty(4, 8, 2, 3, "cpu")
+    one = nq.PackedStore(ok.codes[:, :, ::2], ok.meta[:, :, ::2], 3)
+    assert nq._packed(one).meta == ok.meta.data_ptr()
+    with pytest.raises(ValueError):
+        nq._packed(ok, 0)  # a store of the host beside tensors of a device

@@ -41,11 +41,13 @@
 // is rotated.  Registers are moved to the softmax warpgroups, which hold a sum
 // per query row.  The work of a launch is split over the tokens (flash
 // decoding) to fill the 148 SMs; tree_combine_kernel merges the splits, applies
-// H and attends the draft nodes in fp32.
+// H and attends the draft nodes in fp32 on the CUDA cores, a warp per row: 1.43
+// of the 2.05 ms that 1024 nodes x 4 heads take over 16 384 tokens of 8 KV heads.
 //
-// What bounds it: the instructions of the warps that unpack and rotate (a
-// 64-column call issues in 68 % of the cycles, a third of that in waits; tensor
-// pipe 20 %, DRAM below 10 %).  Per call with 8 KV heads, 3-bit keys and 2-bit
+// What bounds it: the instructions of the warps that unpack and rotate (16, 64
+// and 128 columns take 2890, 3340 and 4380 cycles per tile and issue in 77, 73
+// and 64 % of the cycles, part of it polls of the waits; tensor pipe 14 to 29 %,
+// DRAM 9 to 15 %).  Per call with 8 KV heads, 3-bit keys and 2-bit
 // values: 32 units x 13 147 tokens, one node of 4 heads (16 columns), 350 us
 // against 45 us for the bytes alone (296 MB at 6567 GB/s); a tree of 64 nodes x
 // 4 heads over 131 072 tokens, 340 to 360 us, 380 to 400 TFLOP/s of the attention's own
@@ -1210,8 +1212,8 @@ struct TreePlan {
 // least time together.  A tile takes 31, 33, 41 and 59 units with 16, 32, 64
 // and 128 columns (measured on 32 x 8 x 13 147 tokens: 306, 330, 405, 592 us of
 // this kernel; below 64 columns the keys are the work), so two blocks of 64
-// lose to one of 128, and three to two (160 rows on that shape: 1255 against
-// 1125 us per call).
+// lose to one of 128, and three to two (160 rows on that shape: 1200 against
+// 1100 us per call; 132 rows, 1180 against 1075).
 // Splits: the launch costs (waves of 148 CTAs) * (tiles per CTA + setup, about
 // three tiles); the smallest cost, the fewest splits among equals.  Units that
 // may hold fewer than n tokens (their lengths are on the device) even out only

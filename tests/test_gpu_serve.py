@@ -1057,3 +1057,58 @@ def test_norm_rope_large_and_small_rows(nq, size, dtype):
     q, _ = nq.nq_qk_norm_rope(x, None, tab, 40, eps=0.0)
     ref, y = ref_norm(x, None, 0.0, pos, 1e4)
     assert (q.double() - ref).abs().le(norm_bound(ref, y, dtype)).all()
+
+
+def test_encode_and_norm_at_offsets_past_32_bits(nq):
+    """Rows written to the last pages of a store of more than 2^31 code words, and
+    heads normed in place in a buffer of more than 2^31 elements."""
+    g = gen(97)
+    H, P = 8, 64
+    pages = (2 ** 31 + 2 ** 23) // (H * P * 12)
+    ks, vs = nq.PackedStore.empty(pages, H, P, 3), nq.PackedStore.empty(pages, H, P, 2)
+    K, V = (torch.randn(H, 5, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    tab = nq.rope_tables(1e4, 5)
+    slot = [pages * P - 1, pages * P - 64, 0, pages * P - 130, pages * P]
+    nq.nq_encode_slots(K, V, ks, vs, i32(slot), i32(range(5)), tab, 5)
+    k1, v1 = nq.PackedStore.empty(1, H, 5, 3), nq.PackedStore.empty(1, H, 5, 2)
+    nq.nq_encode(K[None], V[None], k1, v1, 5, tab, 5)
+    for r in range(4):
+        for a, b in ((ks, k1), (vs, v1)):
+            assert torch.equal(a.codes[slot[r] // P, :, slot[r] % P], b.codes[0, :, r])
+            assert torch.equal(a.meta[slot[r] // P, :, slot[r] % P], b.meta[0, :, r])
+    del ks, vs
+    far = 2 ** 31 + 2 ** 20
+    buf = torch.zeros(far + 4096, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((2, 3, 5, D), (far, 5 * D, D, 1))
+    x.copy_(torch.randn(2, 3, 5, D, generator=g, device="cuda"))
+    want, _ = nq.nq_qk_norm_rope(x.contiguous(), None, tab, 5)
+    nq.nq_qk_norm_rope(x, None, tab, 5, q_out=x)
+    assert torch.equal(x, want)
+
+
+def test_calls_under_way_on_two_streams(nq):
+    """Two steps at once, each on its own stream with its own workspace: neither
+    changes the other's bits."""
+    g = gen(98)
+    U, H, G, M, n = 6, 8, 4, 12, 3000
+    ks, vs = fill_store(nq, U, H, n, 3, 1), fill_store(nq, U, H, n, 2, 2)
+    tab = nq.rope_tables(1e4, n)
+    pos = torch.arange(M, dtype=torch.int32, device="cuda").expand(U, M).contiguous()
+    x = [torch.randn(U, M, (G + 2) * H, D, generator=g, device="cuda").to(torch.bfloat16).permute(0, 2, 1, 3)
+         for _ in range(2)]
+    lens = [i32([n, 5, 1700, 0, 128, 2999]), None]
+
+    def step(i, stream):
+        q, k = nq.nq_qk_norm_rope(x[i][:, :G * H], x[i][:, G * H:(G + 1) * H], tab, n, positions=pos, stream=stream)
+        return nq.nq_tree_attend(q, k, x[i][:, (G + 1) * H:], ks, vs, n, tab, n, lens=lens[i], stream=stream)
+
+    want = [step(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(15):
+        for i in range(2):
+            got[i].append(step(i, streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])
+    assert nq.device_error() == 0

@@ -534,6 +534,7 @@ def nq_entropy_decode(coded: EntropyCoded, out: PackedStore, slot0: int = 0, str
 # integers go to ctypes as pointers, and every check is one comparison.
 BF16, F32 = 0, 1
 _TYPES = {torch.bfloat16: BF16, torch.float32: F32}
+_WORDS = (torch.int32, torch.uint32)  # of a packed store
 _NO_CONTEXT = contextlib.nullcontext()
 _NO_STRIDES = KVStrides(0, 0, 0)
 
@@ -607,8 +608,8 @@ def _packed(s: PackedStore, idx: int = -1) -> Packed:
     checked: units and heads anywhere, the slots of a head side by side."""
     c, m, w = s.codes, s.meta, 4 * s.bits
     u, h, t = m.stride()
-    if c.dtype is not torch.int32 or m.dtype is not torch.int32 or c.get_device() != idx or m.get_device() != idx:
-        raise ValueError("codes and meta of a store must be int32 tensors on the tensors' device")
+    if c.dtype not in _WORDS or m.dtype not in _WORDS or c.get_device() != idx or m.get_device() != idx:
+        raise ValueError("codes and meta of a store must be 32-bit words on the tensors' device")
     if c.shape != (*m.shape, w) or ((c.stride() != (u * w, h * w, w, 1) or t != 1) and (
             m.shape[2] > 1 or c.stride()[:2] != (u * w, h * w) or c.stride(3) != 1)):
         raise ValueError("codes and meta of a store must be laid out alike, slots side by side")

@@ -258,3 +258,8 @@ def test_binding_takes_a_store_of_one_slot_with_any_slot_stride(nq):
     assert nq._packed(one).meta == ok.meta.data_ptr()
     with pytest.raises(ValueError):
         nq._packed(ok, 0)  # a store of the host beside tensors of a device
+
+
+def test_binding_takes_stores_of_unsigned_words(nq):
+    ok = nq.PackedStore.empty(4, 8, 2, 3, "cpu")
+    assert nq._packed(nq.PackedStore(ok.codes.view(torch.uint32), ok.meta.view(torch.uint32), 3)).bits == 3
